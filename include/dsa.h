@@ -149,12 +149,29 @@ typedef struct dsa_attn_in {
   dsa_kv_layout kv_layout;
 } dsa_attn_in;
 
+/* A latent KV cache in 8 bits. Row values are decode(code) * 2^e: e4m3 codes
+ * and one exponent e in [-64, 63] for every block of 64 tokens -- a page
+ * (PAGED), or rows 64 j .. 64 j + 63 (CONTIGUOUS). The latent row is the one
+ * KV head that all query heads share, so this is one scale per block and head.
+ * The scale is a power of two because moving a code to a larger exponent is
+ * then exact except among e4m3's subnormals, so a page can be re-scaled, and
+ * rows of several pages merged, without rounding them again. */
+typedef struct dsa_kv8_cache {
+  uint8_t* codes;       /* CONTIGUOUS: [n_keys, 576]; PAGED: [num_pages, 64, 576]; 16-byte aligned */
+  int64_t ld;           /* bytes between rows (>= 576, a multiple of 16) */
+  int8_t* exps;         /* CONTIGUOUS: [ceil(n_keys / 64)]; PAGED: [num_pages] */
+  int32_t n_keys;       /* CONTIGUOUS: rows, the new ones included; PAGED: ignored */
+  dsa_kv_layout kv;     /* q_seq and q_pos are ignored; PAGED: n_seq >= 1 */
+} dsa_kv8_cache;
+
 typedef enum dsa_op {
   DSA_OP_INDEXER_SCORES = 0,
   DSA_OP_TOPK = 1,
   DSA_OP_SPARSE_MQA = 2,
   DSA_OP_FORWARD = 3,
-  DSA_OP_SELECT = 4
+  DSA_OP_SELECT = 4,
+  DSA_OP_KV8_MQA = 5,
+  DSA_OP_KV8_ACCUMULATE = 6
 } dsa_op;
 
 /* Step 1 alone: lightning-indexer scores for selected query rows.
@@ -282,6 +299,90 @@ DSA_API dsa_status dsa_sparse_mqa_bwd(const dsa_attn_in* in, const int32_t* idx,
                                       int32_t k, const void* out, const float* lse,
                                       const void* d_out, void* d_q, float* d_kv, int64_t ld_dkv,
                                       float* delta, dsa_stream_t stream);
+
+/* ---- The latent cache in 8 bits: written, read, weighed and evicted ---- */
+
+/* Quantises new latent rows into the cache (decode: one row a sequence;
+ * prefill: a run of rows a sequence).
+ * rows: [n_rows, 576] DSA_BF16 or DSA_F32, ld_rows elements apart (16-byte
+ * aligned rows). PAGED: sequence b takes rows cu_rows[b] .. cu_rows[b+1]-1
+ * (device array of n_seq + 1 ascending offsets, from 0 to n_rows) as its
+ * newest tokens, at positions ctx_lens[b] - (cu_rows[b+1] - cu_rows[b]) ..
+ * ctx_lens[b] - 1; cu_rows NULL: one row a sequence (n_rows == n_seq).
+ * CONTIGUOUS: the rows go to the end, n_keys - n_rows .. n_keys - 1; cu_rows
+ * must be NULL.
+ * A block that receives rows gets e = the smallest exponent in [-64, 63] with
+ * amax <= 448 * 2^e over the block's new finite values; if the block holds
+ * earlier rows (those before its first new one), e is not below their exponent
+ * and their codes are rewritten to it. Codes round to nearest even; larger
+ * values saturate at 448 * 2^e, NaN stays NaN. Rows of the block behind the
+ * last new one are left as they were. A sequence whose run does not fit its
+ * length, or a page id out of range, is reported as DSA_ERR_DEVICE_BOUNDS and
+ * skipped. Sequences of one call must not share the pages that they write.
+ * No workspace. */
+DSA_API dsa_status dsa_kv8_store(const dsa_kv8_cache* cache, int32_t rows_dtype,
+                                 const void* rows, int64_t ld_rows, const int32_t* cu_rows,
+                                 int32_t n_rows, dsa_stream_t stream);
+
+/* MQA attention over the 8-bit cache, over a selection or over every preceding
+ * key. in: as for dsa_sparse_mqa_fwd with DSA_BF16 queries and output, any 1 <=
+ * heads <= 128, d_qk = 576, d_v = 512; in->kv holds the e4m3 codes (ld_kv in
+ * bytes, a multiple of 16), kv_exp the exponents, in->kv_layout where they lie.
+ * idx, ld_idx, k: the selection, with the rules of dsa_sparse_mqa_fwd; or idx
+ * NULL (k, ld_idx ignored): query i attends to keys 0..pos. A query without
+ * any key gets a zero output and lse = -INFINITY. out: [n_q, heads, 512]
+ * contiguous, 16-byte aligned; lse: [n_q, heads] or NULL.
+ * Codes past a query's position are never read into a result, whatever they
+ * hold; an infinity or NaN in a query head makes that head's output NaN.
+ * Workspace: dsa_workspace_size(DSA_OP_KV8_MQA, NULL, in, 0, 0, k) with k 0
+ * for idx NULL; its contents are not kept between calls. */
+DSA_API dsa_status dsa_kv8_mqa_fwd(const dsa_attn_in* in, const int8_t* kv_exp,
+                                   const int32_t* idx, int64_t ld_idx, int32_t k, void* out,
+                                   float* lse, void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/* Each cached token's running attention weight, for eviction. For every
+ * sequence b and position s < its length:
+ *   acc[b*ld_acc + s] = decay * acc[b*ld_acc + s] + sum_i w[i,s],
+ *   w[i,s] = (1/heads) sum_h exp(scale * q[i,h] . kv[s] - lse[i,h])
+ * over b's queries i in ascending order, with the keys that query i attends to
+ * (its selection, or 0..pos with idx NULL; an entry that repeats a key counts
+ * again). CONTIGUOUS: one sequence of n_keys. in, kv_exp, idx, k: as given to
+ * dsa_kv8_mqa_fwd; lse: [n_q, heads], its log-sum-exp (a head with lse =
+ * -INFINITY adds nothing). decay is finite and in [0, 1]. acc: n_seq rows
+ * (n_seq 0: n_q rows), ld_acc >= max_pages*64 (PAGED) or n_keys. The sums run
+ * in a fixed order: the same call gives the same bits.
+ * Workspace: dsa_workspace_size(DSA_OP_KV8_ACCUMULATE, NULL, in, 0, 0, k). */
+DSA_API dsa_status dsa_kv8_accumulate(const dsa_attn_in* in, const int8_t* kv_exp,
+                                      const int32_t* idx, int64_t ld_idx, int32_t k,
+                                      const float* lse, float decay, float* acc, int64_t ld_acc,
+                                      void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/* Evicts tokens by accumulated weight, PAGED caches only: every sequence b of
+ * cache->kv keeps m = min(budget, ctx_lens[b]) tokens -- all of them, or the
+ * first `sink`, the last `recent` and between those the budget - sink - recent
+ * with the largest acc (ties to the lower position, -0.0 equal to +0.0, NaN
+ * below every number) -- and moves them in their order into the pages
+ * dst_table[b*ld_dst + 0 .. ceil(m/64)-1], a copy that leaves the old pages as
+ * they are (so pages shared between sequences stay whole): the caller then
+ * points the block table at the new pages and frees the old ones. A new page's
+ * exponent is the largest among the old exponents of its rows.
+ * idx_codes ([num_pages, 64, 128] bytes, ld_idx_codes >= 128 apart, a multiple of
+ * 16) and idx_scales ([num_pages * 64]): the indexer's key cache in the same
+ * pages, moved along; both NULL to leave it out. new_lens[b] = m (it may be the
+ * array ctx_lens itself); kept[b*ld_kept + 0..budget-1]: the kept positions,
+ * ascending, then -1; acc_out[b*ld_acc_out + 0..m-1]: their weights, later
+ * columns left as they were (acc_out must not overlap acc).
+ * 0 <= sink, recent; 1 <= budget, sink + recent <= budget <= 64 * ld_dst <=
+ * 64 * 2^24; ld_acc >= max_pages*64; ld_kept, ld_acc_out >= budget. dst pages must
+ * be distinct and none of them a page that the call reads. A length or page id
+ * out of range is reported as DSA_ERR_DEVICE_BOUNDS; its sequence (length: m =
+ * 0) or its rows are skipped. No workspace. */
+DSA_API dsa_status dsa_kv8_evict(const dsa_kv8_cache* cache, uint8_t* idx_codes,
+                                 int64_t ld_idx_codes, float* idx_scales, const float* acc,
+                                 int64_t ld_acc, int32_t budget, int32_t sink, int32_t recent,
+                                 const int32_t* dst_table, int64_t ld_dst, int32_t* new_lens,
+                                 int32_t* kept, int64_t ld_kept, float* acc_out,
+                                 int64_t ld_acc_out, dsa_stream_t stream);
 
 /* Workspace bytes for `op` with these inputs (arguments an op does not use may
  * be NULL/0). The workspace must be 256-byte aligned device memory. */

@@ -246,6 +246,79 @@ dsa_status check_attn(const dsa_attn_in* in) {
   return DSA_ERR_UNSUPPORTED;
 }
 
+// Attention over the 8-bit cache: bf16 queries of up to 128 heads, e4m3 codes.
+dsa_status check_kv8_attn(const dsa_attn_in* in, const int8_t* kv_exp, const int32_t* idx,
+                          int64_t ld_idx, int32_t k) {
+  if (in == nullptr || kv_exp == nullptr) return DSA_ERR_INVALID_ARG;
+  DSA_TRY(check_layout(in->kv_layout, in->n_q, in->n_keys));
+  if (in->q == nullptr || in->kv == nullptr) return DSA_ERR_INVALID_ARG;
+  if (!(in->scale > 0.f) || !std::isfinite(in->scale)) return DSA_ERR_INVALID_ARG;
+  if (in->dtype != DSA_BF16 || in->d_qk != 576 || in->d_v != 512 || in->v != nullptr)
+    return DSA_ERR_UNSUPPORTED;
+  if (in->heads < 1) return DSA_ERR_INVALID_ARG;
+  if (in->heads > 128) return DSA_ERR_UNSUPPORTED;
+  if (in->ld_q < static_cast<int64_t>(in->heads) * 576 || in->ld_kv < 576)
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned16(in->q) || !aligned16(in->kv) || (in->ld_q * 2) % 16 || in->ld_kv % 16)
+    return DSA_ERR_INVALID_ARG;
+  if (idx != nullptr && (k < 1 || k > kKMax || ld_idx < k)) return DSA_ERR_INVALID_ARG;
+  return DSA_OK;
+}
+
+// Keys of the longest query a call may meet.
+int64_t kv8_max_keys(const dsa_attn_in& in, int32_t k) {
+  if (k > 0) return k;
+  return in.kv_layout.kind == DSA_KV_PAGED ? int64_t(in.kv_layout.max_pages) * kPage : in.n_keys;
+}
+
+dsa::Kv8AttnArgs kv8_attn_args(const dsa_attn_in& in, const int8_t* kv_exp, const int32_t* idx,
+                               int64_t ld_idx, int32_t k, DeviceInfo* dev) {
+  dsa::Kv8AttnArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(in.q);
+  a.ld_q = in.ld_q;
+  a.heads = in.heads;
+  a.kv = static_cast<const uint8_t*>(in.kv);
+  a.ld_kv = in.ld_kv;
+  a.exps = kv_exp;
+  a.idx = idx;
+  a.ld_idx = ld_idx;
+  a.k = idx != nullptr ? k : 0;
+  a.keys = key_side(in.kv_layout, in.n_q, in.n_keys);
+  a.scale_log2 = in.scale * 1.4426950408889634f;
+  a.status = dev->status;
+  return a;
+}
+
+dsa_status check_kv8_cache(const dsa_kv8_cache* c) {
+  if (c == nullptr || c->codes == nullptr || c->exps == nullptr) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(c->codes) || c->ld < 576 || c->ld % 16) return DSA_ERR_INVALID_ARG;
+  if (c->kv.kind == DSA_KV_CONTIGUOUS) return c->n_keys < 1 ? DSA_ERR_INVALID_ARG : DSA_OK;
+  if (c->kv.kind == DSA_KV_PAGED && c->kv.n_seq < 1) return DSA_ERR_INVALID_ARG;
+  dsa_kv_layout kv = c->kv;   // queries play no part here
+  kv.q_seq = nullptr;
+  return check_layout(kv, kv.n_seq, 0);
+}
+
+dsa::Kv8Pages kv8_pages(const dsa_kv8_cache& c) {
+  dsa::Kv8Pages p{};
+  p.codes = c.codes;
+  p.ld = c.ld;
+  p.exps = c.exps;
+  if (c.kv.kind == DSA_KV_PAGED) {
+    p.table = c.kv.block_table;
+    p.ld_table = c.kv.ld_block_table;
+    p.max_pages = c.kv.max_pages;
+    p.num_pages = c.kv.num_pages;
+    p.ctx_lens = c.kv.ctx_lens;
+    p.n_seq = c.kv.n_seq;
+  } else {
+    p.max_pages = p.num_pages = c.n_keys / kPage + (c.n_keys % kPage != 0);
+    p.n_keys = c.n_keys;
+    p.n_seq = 1;
+  }
+  return p;
+}
+
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Query rows per indexer launch inside the fused prefill. The score block of
@@ -440,6 +513,15 @@ dsa_status run_select(const dsa_indexer_in& ind, int32_t k, int32_t* idx, int64_
   return DSA_OK;
 }
 
+// A launcher that issues several kernels and says how many.
+template <typename F>
+dsa_status kv8_launched(F launch) {
+  int n = 0;
+  const cudaError_t e = launch(&n);
+  g_launches.fetch_add(n, std::memory_order_relaxed);
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -578,7 +660,6 @@ DSA_API dsa_status dsa_sparse_mqa_bwd(const dsa_attn_in* in, const int32_t* idx,
 DSA_API dsa_status dsa_workspace_size(int32_t op, const dsa_indexer_in* indexer,
                                       const dsa_attn_in* attn, int32_t n_rows, int32_t n_cols,
                                       int32_t k, size_t* bytes) {
-  (void)attn;
   (void)n_rows;
   (void)n_cols;
   if (bytes == nullptr) return DSA_ERR_INVALID_ARG;
@@ -594,6 +675,18 @@ DSA_API dsa_status dsa_workspace_size(int32_t op, const dsa_indexer_in* indexer,
       if (k < 1 || k > kKMax) return DSA_ERR_INVALID_ARG;
       const ForwardPlan p = forward_plan(*indexer, k);
       *bytes = p.scores_bytes + (op == DSA_OP_FORWARD ? p.idx_bytes : 0);
+      return DSA_OK;
+    }
+    case DSA_OP_KV8_MQA:
+    case DSA_OP_KV8_ACCUMULATE: {
+      static const int8_t any_exp = 0;    // only the sizes are looked at
+      static const int32_t any_idx = 0;
+      if (k < 0) return DSA_ERR_INVALID_ARG;
+      DSA_TRY(check_kv8_attn(attn, &any_exp, k > 0 ? &any_idx : nullptr, k, k));
+      const int64_t keys = kv8_max_keys(*attn, k);
+      *bytes = op == DSA_OP_KV8_MQA
+                   ? dsa::kv8_mqa_workspace(attn->n_q, attn->heads, keys)
+                   : round256(static_cast<size_t>(attn->n_q) * keys * sizeof(float));
       return DSA_OK;
     }
     default:
@@ -668,6 +761,124 @@ DSA_API dsa_status dsa_select_scored(const dsa_indexer_in* indexer, int32_t k, i
                     reinterpret_cast<cudaStream_t>(stream), sel_scores, ld_sel);
 }
 
+DSA_API dsa_status dsa_kv8_store(const dsa_kv8_cache* cache, int32_t rows_dtype,
+                                 const void* rows, int64_t ld_rows, const int32_t* cu_rows,
+                                 int32_t n_rows, dsa_stream_t stream) {
+  NvtxRange range("dsa_kv8_store");
+  DSA_TRY(check_kv8_cache(cache));
+  if (rows_dtype != DSA_BF16 && rows_dtype != DSA_F32) return DSA_ERR_UNSUPPORTED;
+  const int64_t elt = rows_dtype == DSA_F32 ? 4 : 2;
+  if (rows == nullptr || n_rows < 1 || ld_rows < 576 || !aligned16(rows) || (ld_rows * elt) % 16)
+    return DSA_ERR_INVALID_ARG;
+  const bool paged = cache->kv.kind == DSA_KV_PAGED;
+  if (!paged && (cu_rows != nullptr || n_rows > cache->n_keys)) return DSA_ERR_INVALID_ARG;
+  if (paged && cu_rows == nullptr && n_rows != cache->kv.n_seq) return DSA_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  DSA_TRY(device_info(&dev));
+  dsa::Kv8StoreArgs a{};
+  a.c = kv8_pages(*cache);
+  a.rows = rows;
+  a.ld_rows = ld_rows;
+  a.cu = cu_rows;
+  a.n_rows = n_rows;
+  a.status = dev->status;
+  DSA_LAUNCH(dsa::launch_kv8_store(a, rows_dtype == DSA_F32, dev->num_sms,
+                                   reinterpret_cast<cudaStream_t>(stream)));
+  return DSA_OK;
+}
+
+DSA_API dsa_status dsa_kv8_mqa_fwd(const dsa_attn_in* in, const int8_t* kv_exp,
+                                   const int32_t* idx, int64_t ld_idx, int32_t k, void* out,
+                                   float* lse, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+  NvtxRange range("dsa_kv8_mqa_fwd");
+  DSA_TRY(check_kv8_attn(in, kv_exp, idx, ld_idx, k));
+  if (out == nullptr || !aligned16(out)) return DSA_ERR_INVALID_ARG;
+  const int64_t keys = kv8_max_keys(*in, idx != nullptr ? k : 0);
+  const size_t need = dsa::kv8_mqa_workspace(in->n_q, in->heads, keys);
+  if (need > 0 && (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < need))
+    return DSA_ERR_WORKSPACE_TOO_SMALL;
+  DeviceInfo* dev = nullptr;
+  DSA_TRY(device_info(&dev));
+  dsa::Kv8AttnArgs a = kv8_attn_args(*in, kv_exp, idx, ld_idx, k, dev);
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.ws = ws;
+  return kv8_launched([&](int* n) {
+    return dsa::launch_kv8_mqa(a, dev->num_sms, n, reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+DSA_API dsa_status dsa_kv8_accumulate(const dsa_attn_in* in, const int8_t* kv_exp,
+                                      const int32_t* idx, int64_t ld_idx, int32_t k,
+                                      const float* lse, float decay, float* acc, int64_t ld_acc,
+                                      void* ws, size_t ws_bytes, dsa_stream_t stream) {
+  NvtxRange range("dsa_kv8_accumulate");
+  DSA_TRY(check_kv8_attn(in, kv_exp, idx, ld_idx, k));
+  if (lse == nullptr || acc == nullptr || !(decay >= 0.f && decay <= 1.f))
+    return DSA_ERR_INVALID_ARG;
+  if (ld_acc < kv8_max_keys(*in, 0)) return DSA_ERR_INVALID_ARG;
+  const int64_t cols = kv8_max_keys(*in, idx != nullptr ? k : 0);
+  const size_t need = round256(static_cast<size_t>(in->n_q) * cols * sizeof(float));
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < need)
+    return DSA_ERR_WORKSPACE_TOO_SMALL;
+  DeviceInfo* dev = nullptr;
+  DSA_TRY(device_info(&dev));
+  dsa::Kv8WeightArgs a{};
+  a.attn = kv8_attn_args(*in, kv_exp, idx, ld_idx, k, dev);
+  a.lse = lse;
+  a.w = static_cast<float*>(ws);
+  a.n_cols = static_cast<int32_t>(cols);
+  a.decay = decay;
+  a.acc = acc;
+  a.ld_acc = ld_acc;
+  return kv8_launched([&](int* n) {
+    return dsa::launch_kv8_accumulate(a, dev->num_sms, n, reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+DSA_API dsa_status dsa_kv8_evict(const dsa_kv8_cache* cache, uint8_t* idx_codes,
+                                 int64_t ld_idx_codes, float* idx_scales, const float* acc,
+                                 int64_t ld_acc, int32_t budget, int32_t sink, int32_t recent,
+                                 const int32_t* dst_table, int64_t ld_dst, int32_t* new_lens,
+                                 int32_t* kept, int64_t ld_kept, float* acc_out,
+                                 int64_t ld_acc_out, dsa_stream_t stream) {
+  NvtxRange range("dsa_kv8_evict");
+  DSA_TRY(check_kv8_cache(cache));
+  if (cache->kv.kind != DSA_KV_PAGED) return DSA_ERR_UNSUPPORTED;
+  if ((idx_codes == nullptr) != (idx_scales == nullptr)) return DSA_ERR_INVALID_ARG;
+  if (idx_codes != nullptr && (!aligned16(idx_codes) || ld_idx_codes < 128 || ld_idx_codes % 16))
+    return DSA_ERR_INVALID_ARG;
+  if (acc == nullptr || dst_table == nullptr || new_lens == nullptr || kept == nullptr ||
+      acc_out == nullptr || budget < 1 || sink < 0 || recent < 0 ||
+      int64_t(sink) + recent > budget || ld_dst > (int64_t(1) << 24) ||
+      budget > ld_dst * kPage || ld_acc < int64_t(cache->kv.max_pages) * kPage ||
+      ld_kept < budget || ld_acc_out < budget)
+    return DSA_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  DSA_TRY(device_info(&dev));
+  dsa::Kv8EvictArgs a{};
+  a.c = kv8_pages(*cache);
+  a.idx_codes = idx_codes;
+  a.ld_idx = ld_idx_codes;
+  a.idx_scales = idx_scales;
+  a.acc = acc;
+  a.ld_acc = ld_acc;
+  a.budget = budget;
+  a.sink = sink;
+  a.recent = recent;
+  a.dst_table = dst_table;
+  a.ld_dst = ld_dst;
+  a.new_lens = new_lens;
+  a.kept = kept;
+  a.ld_kept = ld_kept;
+  a.acc_out = acc_out;
+  a.ld_acc_out = ld_acc_out;
+  a.status = dev->status;
+  return kv8_launched([&](int* n) {
+    return dsa::launch_kv8_evict(a, n, reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
 DSA_API int64_t dsa_launch_counter(void) { return g_launches.load(); }
 
 DSA_API dsa_status dsa_set_wait_limit_ns(int64_t ns) {
@@ -703,7 +914,7 @@ DSA_API const char* dsa_status_string(dsa_status s) {
 
 DSA_API int32_t dsa_last_cuda_error(void) { return t_last_cuda_error; }
 
-DSA_API int32_t dsa_version(void) { return 201; }
+DSA_API int32_t dsa_version(void) { return 300; }
 
 }  // extern "C"
 

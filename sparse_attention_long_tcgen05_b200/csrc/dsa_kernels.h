@@ -186,6 +186,90 @@ struct KlArgs {
 
 cudaError_t launch_indexer_kl(const KlArgs& a, cudaStream_t stream);
 
+// ---------------------------------------------------------------- 8-bit latent cache
+
+// Where the cache's rows live: a page id per 64 tokens of a sequence, or the
+// block number itself (contiguous: table null, one sequence of n_keys).
+struct Kv8Pages {
+  uint8_t* codes;           // [rows, ld] e4m3, row = page * 64 + slot
+  int64_t ld;               // bytes between rows
+  int8_t* exps;             // [pages]
+  const int32_t* table;     // [n_seq, ld_table] or null
+  int64_t ld_table;
+  int32_t max_pages;        // table columns (contiguous: blocks)
+  int32_t num_pages;
+  const int32_t* ctx_lens;  // [n_seq] or null (contiguous: n_keys)
+  int32_t n_keys;
+  int32_t n_seq;
+};
+
+struct Kv8StoreArgs {
+  Kv8Pages c;
+  const void* rows;         // [n_rows, ld_rows] bf16 or f32
+  int64_t ld_rows;
+  const int32_t* cu;        // [n_seq + 1] or null (paged: a row per sequence)
+  int32_t n_rows;
+  int32_t rows_per_cta;
+  int* status;
+};
+
+cudaError_t launch_kv8_store(const Kv8StoreArgs& a, bool f32, int num_sms, cudaStream_t stream);
+
+struct Kv8AttnArgs {
+  const __nv_bfloat16* q;   // [n_q, heads, 576], query tokens ld_q apart
+  int64_t ld_q;
+  int32_t heads;
+  const uint8_t* kv;        // codes, rows ld_kv bytes apart
+  int64_t ld_kv;
+  const int8_t* exps;
+  const int32_t* idx;       // [n_q, ld_idx], or null: every key 0..pos
+  int64_t ld_idx;
+  int32_t k;
+  KeySide keys;
+  float scale_log2;         // softmax scale * log2(e)
+  __nv_bfloat16* out;       // [n_q, heads, 512]
+  float* lse;               // [n_q, heads] or null
+  void* ws;
+  int* status;
+};
+
+// Workspace bytes of launch_kv8_mqa; max_keys: keys of the longest query.
+size_t kv8_mqa_workspace(int32_t n_q, int32_t heads, int64_t max_keys);
+cudaError_t launch_kv8_mqa(const Kv8AttnArgs& a, int num_sms, int* launches, cudaStream_t stream);
+
+struct Kv8WeightArgs {
+  Kv8AttnArgs attn;         // out, lse and ws unused
+  const float* lse;         // [n_q, heads]
+  float* w;                 // [n_q, n_cols] workspace: mean over the heads
+  int32_t n_cols;           // k, or the keys of the longest query
+  float decay;
+  float* acc;               // [n_seq, ld_acc]
+  int64_t ld_acc;
+};
+
+cudaError_t launch_kv8_accumulate(const Kv8WeightArgs& a, int num_sms, int* launches,
+                                  cudaStream_t stream);
+
+struct Kv8EvictArgs {
+  Kv8Pages c;
+  uint8_t* idx_codes;       // [num_pages * 64, ld_idx] or null
+  int64_t ld_idx;
+  float* idx_scales;        // [num_pages * 64] or null
+  const float* acc;
+  int64_t ld_acc;
+  int32_t budget, sink, recent;
+  const int32_t* dst_table;
+  int64_t ld_dst;
+  int32_t* new_lens;
+  int32_t* kept;
+  int64_t ld_kept;
+  float* acc_out;
+  int64_t ld_acc_out;
+  int* status;
+};
+
+cudaError_t launch_kv8_evict(const Kv8EvictArgs& a, int* launches, cudaStream_t stream);
+
 // Sequence and position of paged query qi (the rule of the ABI's PAGED
 // layout): the sequence is q_seq[qi] (qi when q_seq is null), whose ctx_lens
 // cached tokens include the query's own; the position is q_pos[qi] (ctx - 1

@@ -30,12 +30,14 @@ DSA_KV_CONTIGUOUS, DSA_KV_PAGED = 0, 1
 DSA_OP_INDEXER_SCORES, DSA_OP_TOPK, DSA_OP_SPARSE_MQA, DSA_OP_FORWARD = 0, 1, 2, 3
 
 DSA_OP_SELECT = 4
+DSA_OP_KV8_MQA, DSA_OP_KV8_ACCUMULATE = 5, 6
 
 EXPORTED = ["dsa_indexer_scores", "dsa_topk", "dsa_sparse_mqa_fwd", "dsa_select", "dsa_forward",
             "dsa_workspace_size", "dsa_check_status", "dsa_status_string",
             "dsa_last_cuda_error", "dsa_launch_counter", "dsa_version", "dsa_select_noalloc",
             "dsa_set_wait_limit_ns", "dsa_dense_mqa_fwd", "dsa_select_scored", "dsa_indexer_kl",
-            "dsa_sparse_mqa_bwd"]
+            "dsa_sparse_mqa_bwd", "dsa_kv8_store", "dsa_kv8_mqa_fwd", "dsa_kv8_accumulate",
+            "dsa_kv8_evict"]
 
 
 class DsaError(RuntimeError):
@@ -70,12 +72,18 @@ class AttnIn(ctypes.Structure):
                 ("kv_layout", KvLayout)]
 
 
+class Kv8Cache(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("ld", ctypes.c_int64), ("exps", ctypes.c_void_p),
+                ("n_keys", ctypes.c_int32), ("kv", KvLayout)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
                           "`python -m sparse_attention_long_tcgen05_b200._build`")
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    F32 = ctypes.c_float
     sig = {
         "dsa_indexer_scores": [ctypes.POINTER(IndexerIn), P, I32, P, I64, I32, P, SZ, P],
         "dsa_topk": [P, I64, P, I32, I32, P, I64, P],
@@ -86,6 +94,11 @@ def _load():
         "dsa_indexer_kl": [ctypes.POINTER(AttnIn), P, I64, I32, P, P, I64, P, P, I64, P],
         "dsa_sparse_mqa_bwd": [ctypes.POINTER(AttnIn), P, I64, I32, P, P, P, P, P, I64, P, P],
         "dsa_forward": [ctypes.POINTER(IndexerIn), ctypes.POINTER(AttnIn), I32, P, P, P, P, SZ, P],
+        "dsa_kv8_store": [ctypes.POINTER(Kv8Cache), I32, P, I64, P, I32, P],
+        "dsa_kv8_mqa_fwd": [ctypes.POINTER(AttnIn), P, P, I64, I32, P, P, P, SZ, P],
+        "dsa_kv8_accumulate": [ctypes.POINTER(AttnIn), P, P, I64, I32, P, F32, P, I64, P, SZ, P],
+        "dsa_kv8_evict": [ctypes.POINTER(Kv8Cache), P, I64, P, P, I64, I32, I32, I32, P, I64, P, P,
+                          I64, P, I64, P],
         "dsa_launch_counter": [],
         "dsa_set_wait_limit_ns": [I64],
         "dsa_select_noalloc": [ctypes.POINTER(IndexerIn), I32, P, I64, P],
@@ -182,6 +195,24 @@ def attn_in(q, kv, scale, d_v, v=None, kv_layout: Optional[KvLayout] = None):
     return _Keep(s, [q, kv, v])
 
 
+def kv8_cache(codes: torch.Tensor, exps: torch.Tensor, kv: Optional[KvLayout] = None,
+              n_keys: Optional[int] = None):
+    """The latent cache in 8 bits: codes uint8 [pages, 64, 576] with a paged
+    layout, or [n_keys, 576]; exps int8, one per page or per 64 rows."""
+    _need(codes, torch.uint8, "kv8_cache: codes")
+    _need(exps, torch.int8, "kv8_cache: exps")
+    lay = kv if kv is not None else KvLayout(DSA_KV_CONTIGUOUS, 0, None, 0, 0, 0, None)
+    n = (n_keys if n_keys is not None else codes.shape[0]) if lay.kind == DSA_KV_CONTIGUOUS else 0
+    s = Kv8Cache(codes.data_ptr(), codes.stride(-2), exps.data_ptr(), n, lay)
+    return _Keep(s, [codes, exps])
+
+
+def _need(t: Optional[torch.Tensor], dtype, what: str):
+    """The C side sees addresses only: another element type would be misread."""
+    if t is not None and t.dtype != dtype:
+        raise DsaError(DSA_ERR_INVALID_ARG, f"{what} must be {dtype}, got {t.dtype}")
+
+
 # ------------------------------------------------------------ the C ABI calls
 
 def dsa_workspace_size(op, ind: Optional[_Keep] = None, attn: Optional[_Keep] = None,
@@ -247,6 +278,63 @@ def dsa_sparse_mqa_bwd(attn: _Keep, idx: torch.Tensor, k: int, out: torch.Tensor
                                   _ptr(out), _ptr(lse), _ptr(d_out), _ptr(d_q), _ptr(d_kv),
                                   d_kv.stride(0), _ptr(delta), _stream(stream)),
            "dsa_sparse_mqa_bwd")
+
+
+def dsa_kv8_store(cache: _Keep, rows: torch.Tensor, cu_rows: Optional[torch.Tensor] = None,
+                  stream=None):
+    """Quantises rows [n, 576] (bf16 or float32) into the cache as the newest
+    tokens: rows cu_rows[b]..cu_rows[b+1]-1 of each sequence b, one row per
+    sequence without cu_rows, or the last n rows of a contiguous cache."""
+    _need(cu_rows, torch.int32, "dsa_kv8_store: cu_rows")
+    if rows.dtype not in (torch.bfloat16, torch.float32):
+        raise DsaError(DSA_ERR_UNSUPPORTED, f"dsa_kv8_store: rows of {rows.dtype}")
+    _check(LIB.dsa_kv8_store(ctypes.byref(cache.struct),
+                             DSA_BF16 if rows.dtype == torch.bfloat16 else DSA_F32, _ptr(rows),
+                             rows.stride(0), _ptr(cu_rows), rows.shape[0], _stream(stream)),
+           "dsa_kv8_store")
+
+
+def dsa_kv8_mqa_fwd(attn: _Keep, kv_exp: torch.Tensor, idx: Optional[torch.Tensor], k: int,
+                    out: torch.Tensor, lse: Optional[torch.Tensor], ws: torch.Tensor,
+                    stream=None):
+    """Attention over the 8-bit cache: attn from attn_in with the codes as kv;
+    idx None (k 0): every preceding key."""
+    _need(kv_exp, torch.int8, "dsa_kv8_mqa_fwd: kv_exp")
+    _need(attn.tensors[1], torch.uint8, "dsa_kv8_mqa_fwd: kv")
+    _check(LIB.dsa_kv8_mqa_fwd(ctypes.byref(attn.struct), _ptr(kv_exp), _ptr(idx),
+                               0 if idx is None else idx.stride(0), k, _ptr(out), _ptr(lse),
+                               _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "dsa_kv8_mqa_fwd")
+
+
+def dsa_kv8_accumulate(attn: _Keep, kv_exp: torch.Tensor, idx: Optional[torch.Tensor], k: int,
+                       lse: torch.Tensor, decay: float, acc: torch.Tensor, ws: torch.Tensor,
+                       stream=None):
+    """acc [n_seq, >= keys] = decay * acc + each cached token's attention weight."""
+    _need(kv_exp, torch.int8, "dsa_kv8_accumulate: kv_exp")
+    _need(attn.tensors[1], torch.uint8, "dsa_kv8_accumulate: kv")
+    _check(LIB.dsa_kv8_accumulate(ctypes.byref(attn.struct), _ptr(kv_exp), _ptr(idx),
+                                  0 if idx is None else idx.stride(0), k, _ptr(lse), decay,
+                                  _ptr(acc), acc.stride(0), _ptr(ws),
+                                  ws.numel() * ws.element_size(), _stream(stream)),
+           "dsa_kv8_accumulate")
+
+
+def dsa_kv8_evict(cache: _Keep, acc: torch.Tensor, budget: int, sink: int, recent: int,
+                  dst_table: torch.Tensor, new_lens: torch.Tensor, kept: torch.Tensor,
+                  acc_out: torch.Tensor, idx_codes: Optional[torch.Tensor] = None,
+                  idx_scales: Optional[torch.Tensor] = None, stream=None):
+    """Keeps `budget` tokens of each sequence and moves them into the pages of
+    dst_table; optionally the indexer's key cache (codes [pages, 64, 128], scales
+    [pages, 64]) along with them."""
+    for t, what in ((dst_table, "dst_table"), (new_lens, "new_lens"), (kept, "kept")):
+        _need(t, torch.int32, "dsa_kv8_evict: " + what)
+    _check(LIB.dsa_kv8_evict(ctypes.byref(cache.struct), _ptr(idx_codes),
+                             0 if idx_codes is None else idx_codes.stride(-2), _ptr(idx_scales),
+                             _ptr(acc), acc.stride(0), budget, sink, recent, _ptr(dst_table),
+                             dst_table.stride(0), _ptr(new_lens), _ptr(kept), kept.stride(0),
+                             _ptr(acc_out), acc_out.stride(0), _stream(stream)),
+           "dsa_kv8_evict")
 
 
 def dsa_select(ind: _Keep, k: int, idx: torch.Tensor, ws: torch.Tensor, stream=None):
