@@ -51,4 +51,233 @@ __device__ __forceinline__ bool kv8_query(const KeySide& ks, int qi, int& seq, i
   return true;
 }
 
+// ------------------------------------------------------------------ tensor-core pieces
+
+// One lane of the (converged) warp: the MMA issuer's branch. Unlike a test of
+// the lane number it leaves the code warp-uniform, so descriptors stay in
+// uniform registers (measured: 48 instead of 55 cycles per small MMA).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Descriptor of a K-major tile with 64-byte rows, 64-byte swizzle (512-byte
+// aligned base; 8-row groups 512 bytes apart).
+__device__ __forceinline__ uint64_t sw64_desc(uint32_t smem_addr) {
+  return (static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu)) | (1ull << 16) |
+         (static_cast<uint64_t>(512 >> 4) << 32) | (1ull << 46) | (4ull << 61);
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
+// N consecutive TMEM columns of this thread's lane.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 8 || N == 16 || N == 32, "");
+  if constexpr (N == 8) tmem_ld8(taddr, r);
+  if constexpr (N == 16) tmem_ld16(taddr, r);
+  if constexpr (N == 32) tmem_ld32(taddr, r);
+}
+
+// 16 bytes global -> shared, or 16 zero bytes (the source is then not read).
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst_smem, const void* src, bool copy) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src),
+               "r"(copy ? 16 : 0)
+               : "memory");
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two floats to e5m2 (round to nearest even, saturating), low byte first; its
+// code is the upper byte of the fp16 of the same value.
+__device__ __forceinline__ uint32_t to_e5m2x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
+}
+
+__device__ __forceinline__ float2 from_e5m2x2(uint32_t codes) {
+  const uint32_t h = __byte_perm(codes, 0, 0x1404);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Sums v[i] over the 32 lanes; lane l gets the sum of element l % N. The order
+// of the additions is fixed.
+template <int N>
+__device__ __forceinline__ float reduce_columns(float (&v)[N], int lane) {
+#pragma unroll
+  for (int off = 16; off >= N; off >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+#pragma unroll
+  for (int off = N / 2; off >= 1; off >>= 1) {
+    const bool up = (lane & off) != 0;
+#pragma unroll
+    for (int i = 0; i < off; ++i) {
+      const float give = up ? v[i] : v[i + off];
+      const float keep = up ? v[i + off] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+    }
+  }
+  return v[0];
+}
+
+// ------------------------------------------------------------------ work split
+
+constexpr int kTile = 128;       // keys of a tile = MMA M (keys on TMEM lanes)
+
+// Tiles of query qi: fixed for a selection, else those of keys 0..pos (one,
+// wholly masked, where there is none).
+__device__ __forceinline__ int kv8_tiles(const KeySide& ks, bool sparse, int k, int qi) {
+  if (sparse) return (k + kTile - 1) / kTile;
+  int seq, pos;
+  kv8_query(ks, qi, seq, pos);
+  return pos / kTile + 1;
+}
+
+// The tiles of all queries in a row, cut into `workers` equal ranges, whatever
+// their queries' lengths.
+struct Kv8Range {
+  int64_t t0, t1;     // this worker's tiles
+  int qi;             // query of tile t0
+  int j0;             // tile t0 within it
+};
+
+// Executed by the whole block (THREADS threads); scratch: THREADS / 32 + 2 words.
+template <int THREADS>
+__device__ __forceinline__ Kv8Range kv8_range(const KeySide& ks, bool sparse, int k, int worker,
+                                              int workers, int64_t* scratch) {
+  Kv8Range r{};
+  if (sparse) {
+    const int64_t per = (k + kTile - 1) / kTile, total = per * ks.n_q;
+    r.t0 = total * worker / workers;
+    r.t1 = total * (worker + 1) / workers;
+    r.qi = static_cast<int>(r.t0 / per);
+    r.j0 = static_cast<int>(r.t0 % per);
+    return r;
+  }
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kW = THREADS / 32;
+  // first the total, then the query that holds tile t0: one pass over the
+  // queries each (the first pass's values are used again when it was the only one)
+  int64_t total = 0, base = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    base = 0;
+    for (int q0 = 0; q0 < ks.n_q; q0 += THREADS) {
+      const int64_t mine = q0 + tid < ks.n_q ? kv8_tiles(ks, false, 0, q0 + tid) : 0;
+      int64_t inc = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += up;
+      }
+      if (lane == 31) scratch[warp] = inc;
+      __syncthreads();
+      int64_t before = base, all = 0;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        if (w < warp) before += scratch[w];
+        all += scratch[w];
+      }
+      const bool only = ks.n_q <= THREADS;
+      if (only) {
+        total = all;
+        r.t0 = total * worker / workers;
+        r.t1 = total * (worker + 1) / workers;
+      }
+      if ((only || pass == 1) && mine > 0 && before + inc - mine <= r.t0 && r.t0 < before + inc) {
+        scratch[kW] = q0 + tid;
+        scratch[kW + 1] = r.t0 - (before + inc - mine);
+      }
+      base += all;
+      __syncthreads();
+      if (only) pass = 1;
+    }
+    total = base;
+    r.t0 = total * worker / workers;
+    r.t1 = total * (worker + 1) / workers;
+  }
+  if (r.t1 > r.t0) {
+    r.qi = static_cast<int>(scratch[kW]);
+    r.j0 = static_cast<int>(scratch[kW + 1]);
+  }
+  __syncthreads();
+  return r;
+}
+
+// ------------------------------------------------------------------ queries as two e4m3 terms
+
+// Writes the queries of `rows` heads (of which `live` exist) as B operands: row
+// h of the tiles is e4m3(q 2^-s), row ROWS + h is e4m3 of 16 times what that left
+// over, with s per head so that the largest element lies in [128, 256). The two
+// terms hold a bf16 element exactly down to 2^-14 of the head's largest one and
+// miss smaller ones by at most 2^-22 of it: the products with the cache's codes
+// are as exact as the codes themselves. Four 128-byte-swizzled chunks of 128
+// columns, 2 ROWS rows each, then the rope columns in 64-byte rows.
+// Returns through set(h, s) the exponent of each head. An infinity or NaN makes
+// the whole head NaN. Warps `warp`, warp + warps, ... take one head at a time.
+template <int ROWS, typename F>
+__device__ __forceinline__ void stage_q8(uint8_t* tile, const __nv_bfloat16* q, int live, int warp,
+                                         int warps, int lane, F set) {
+  constexpr int kChunk = 2 * ROWS * 128;
+  for (int h = warp; h < ROWS; h += warps) {
+    uint32_t w[9];
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(h) * kRow8);
+#pragma unroll
+    for (int i = 0; i < 9; ++i) w[i] = h < live ? __ldg(src + lane + 32 * i) : 0u;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 9; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    m = __reduce_max_sync(0xffffffffu, m);
+    const bool bad = m >= 0x7f80u;
+    const int s = min(max(static_cast<int>(m >> 7) - 127 - 7, -120), 120);
+    const float f = pow2i(-s);
+#pragma unroll
+    for (int i = 0; i < 9; ++i) {
+      const float x = __uint_as_float(w[i] << 16) * f, y = __uint_as_float(w[i] & 0xffff0000u) * f;
+      uint32_t hi = to_e4m3x2(x, y);
+      const float2 b = from_e4m3x2(hi);
+      uint32_t lo = to_e4m3x2((x - b.x) * 16.f, (y - b.y) * 16.f);
+      if (bad) hi = lo = 0x7f7fu;
+      const int col = 2 * (lane + 32 * i);
+      uint8_t* at;
+      int step;                                     // from the first term's row to the second's
+      if (i < 8) {
+        at = tile + (col >> 7) * kChunk + h * 128 + ((((col & 127) >> 4) ^ (h & 7)) << 4);
+        step = ROWS * 128;
+      } else {
+        at = tile + 4 * kChunk + h * 64 + ((((col - 512) >> 4) ^ ((h >> 1) & 3)) << 4);
+        step = ROWS * 64;
+      }
+      *reinterpret_cast<uint16_t*>(at + (col & 15)) = static_cast<uint16_t>(hi);
+      *reinterpret_cast<uint16_t*>(at + step + (col & 15)) = static_cast<uint16_t>(lo);
+    }
+    if (lane == 0) set(h, s);
+  }
+}
+
 }  // namespace dsa

@@ -1,0 +1,181 @@
+// kv8_gather.cuh -- the copying warps of the kernels that read the 8-bit latent
+// cache: rows of a tile's 128 keys into swizzled shared-memory tiles.
+#pragma once
+
+#include "kv8_common.cuh"
+
+namespace dsa {
+
+constexpr int kGatherWarps = 4;      // warp g copies keys 32 g .. 32 g + 31 of a tile
+constexpr int kChunkB = kTile * 128; // 128 columns of a tile's keys: 16 KB
+constexpr int kRopeB = kTile * 64;   // the 64 rope columns: 8 KB
+constexpr int kRopeRing = 2;
+constexpr int kMetaRing = 4;
+constexpr int kInFlight = 4;         // copy groups of a warp that may be pending after an issue
+
+// The ring of a kernel: R chunk slots, two rope slots, and the scale of each
+// key of a tile (2^e, or 0 for a key that does not count).
+template <int R>
+struct __align__(1024) Kv8Ring {
+  uint8_t chunk[R][kChunkB];
+  uint8_t rope[kRopeRing][kRopeB];
+  float key_scale[kMetaRing][kTile];
+  uint64_t full[R], empty[R];
+  uint64_t rope_full[kRopeRing], rope_empty[kRopeRing];
+  uint64_t meta_full[kMetaRing];
+
+  __device__ void init() {
+    for (int i = 0; i < R; ++i) {
+      mbar_init(&full[i], kGatherWarps);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kRopeRing; ++i) {
+      mbar_init(&rope_full[i], kGatherWarps);
+      mbar_init(&rope_empty[i], 1);
+    }
+    for (int i = 0; i < kMetaRing; ++i) mbar_init(&meta_full[i], kGatherWarps);
+  }
+};
+
+// One copying warp. Units of a tile in the order in which the MMAs want them:
+// chunks 0, 1, 2, rope, chunk 3. A unit is released to the MMA issuer once this
+// warp's copies of it have landed, at the latest when kInFlight newer ones have
+// been issued, and always before the warp waits for a slot: the issuer frees
+// slots in order, so nothing that it needs may be held back here.
+template <int R>
+struct Kv8Gather {
+  Kv8Ring<R>& ring;
+  const Kv8AttnArgs& a;
+  int lane, g;             // g: copying warp 0..3
+  uint32_t issued = 0, released = 0;      // units
+  uint32_t n_chunk = 0, n_rope = 0, n_tile = 0;
+  uint32_t rel_chunk = 0, rel_rope = 0;
+
+  __device__ __forceinline__ void release_oldest() {
+    switch (issued - released) {
+      case 1: cp_async_wait_group<0>(); break;
+      case 2: cp_async_wait_group<1>(); break;
+      case 3: cp_async_wait_group<2>(); break;
+      case 4: cp_async_wait_group<3>(); break;
+      default: cp_async_wait_group<4>(); break;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (released % 5 == 3) {
+      if (lane == 0) mbar_arrive(&ring.rope_full[rel_rope % kRopeRing]);
+      ++rel_rope;
+    } else {
+      if (lane == 0) mbar_arrive(&ring.full[rel_chunk % R]);
+      ++rel_chunk;
+    }
+    ++released;
+  }
+
+  // Waits until `bar` has completed the phase of `parity`, releasing what is
+  // pending first.
+  __device__ __forceinline__ bool wait_slot(uint64_t* bar, uint32_t parity) {
+    while (issued != released) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity, 1))) return true;
+      release_oldest();
+    }
+    return mbar_wait_warp(bar, parity, a.status);
+  }
+
+  __device__ __forceinline__ void committed() {
+    cp_async_commit();
+    ++issued;
+    if (issued - released > kInFlight) release_oldest();
+  }
+
+  // Key position of this lane's row in tile j of query qi: p in [0, pos], or -1;
+  // bad: an entry past the query's position.
+  __device__ __forceinline__ int key_of(int qi, int pos, int j, bool& bad) const {
+    const int r = j * kTile + 32 * g + lane;
+    if (a.idx == nullptr) return r <= pos ? r : -1;
+    const int e = r < a.k ? __ldg(a.idx + static_cast<int64_t>(qi) * a.ld_idx + r) : -1;
+    bad = e > pos;
+    return e > pos ? -1 : e;
+  }
+
+  // Tiles [j0, j0 + n) of query qi. False when a wait ran out.
+  __device__ bool run(int qi, int j0, int n) {
+    int seq, pos;
+    const bool q_ok = kv8_query(a.keys, qi, seq, pos);
+    if (!q_ok && lane == 0) report(a.status, DSA_ERR_DEVICE_BOUNDS);
+    bool bad = false, any_bad = false;
+    int p = key_of(qi, pos, j0, bad);
+    any_bad |= bad;
+    int64_t row = p >= 0 ? kv8_row(a.keys, seq, p) : -1;
+    for (int j = j0; j < j0 + n; ++j) {
+      // the next tile's entries are fetched now, its page ids below
+      bool bad_next = false;
+      const int p_next = j + 1 < j0 + n ? key_of(qi, pos, j + 1, bad_next) : -1;
+      if (p >= 0 && row < 0) any_bad = true;      // a page id out of range
+      const bool ok = row >= 0;
+      const uint8_t* src = a.kv + (ok ? row * a.ld_kv : 0);
+      float scale = 0.f;
+      if (ok) scale = pow2i(__ldg(a.exps + (row >> 6)));
+      const uint64_t src_bits = reinterpret_cast<uint64_t>(src);
+      const uint32_t ok_mask = __ballot_sync(0xffffffffu, ok);
+      // chunk copies: instruction i covers rows 4 i .. 4 i + 3 of this warp's 32
+      uint64_t at[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        at[i] = __shfl_sync(0xffffffffu, src_bits, 4 * i + (lane >> 3)) + 16 * (lane & 7);
+      int64_t row_next = -1;
+#pragma unroll
+      for (int u = 0; u < 5; ++u) {
+        if (u == 3) {
+          const uint32_t slot = n_rope % kRopeRing;
+          if (!wait_slot(&ring.rope_empty[slot], ((n_rope / kRopeRing) & 1) ^ 1)) return false;
+          const uint32_t dst = smem_u32(ring.rope[slot]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = 8 * i + (lane >> 2);
+            const uint64_t s = __shfl_sync(0xffffffffu, src_bits, rr) + 512 + 16 * (lane & 3);
+            const int r = 32 * g + rr;
+            cp_async16_or_zero(dst + r * 64 + ((((lane & 3) ^ (r >> 1)) & 3) << 4),
+                               reinterpret_cast<const void*>(s), (ok_mask >> rr) & 1u);
+          }
+          ++n_rope;
+        } else {
+          const int c = u < 3 ? u : 3;
+          const uint32_t slot = n_chunk % R;
+          if (!wait_slot(&ring.empty[slot], ((n_chunk / R) & 1) ^ 1)) return false;
+          if (u == 0) {
+            // the scales: slot n_tile % 4 was read long ago (chunk slots of the
+            // tile before last are only free after its softmax)
+            const uint32_t ms = n_tile % kMetaRing;
+            ring.key_scale[ms][32 * g + lane] = scale;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ring.meta_full[ms]);
+            ++n_tile;
+          }
+          const uint32_t dst = smem_u32(ring.chunk[slot]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = 4 * i + (lane >> 3);
+            const int r = 32 * g + rr;
+            cp_async16_or_zero(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
+                               reinterpret_cast<const void*>(at[i] + 128 * c), (ok_mask >> rr) & 1u);
+          }
+          ++n_chunk;
+        }
+        committed();
+        if (u == 1 && p_next >= 0) row_next = kv8_row(a.keys, seq, p_next);
+      }
+      p = p_next;
+      row = row_next;
+      any_bad |= bad_next;
+    }
+    if (any_bad) report(a.status, DSA_ERR_DEVICE_BOUNDS);
+    return true;
+  }
+
+  __device__ __forceinline__ void drain() {
+    while (issued != released) release_oldest();
+    cp_async_wait_group<0>();
+  }
+};
+
+}  // namespace dsa

@@ -1,114 +1,601 @@
 // kv8_mqa.cu -- MQA attention over the 8-bit latent cache, over a selection or
-// over every preceding key.
+// over every preceding key, on the 5th-generation tensor cores.
 //
 //   O[t,h] = sum_s softmax_s(scale * q[t,h] . kv[s]) * kv[s, 0:512],
 //   kv[s] = decode(codes[s]) * 2^e(block of s)
 //
-// One CTA per (query, head): each warp takes every eighth key, holds the head's
-// query in registers (18 columns a lane), adds the lanes' products and keeps an
-// online softmax of its own over 16 value columns a lane; the warps' partial
-// results are joined in shared memory.
-#include "kv8_common.cuh"
+// Everything runs on kind::f8f6f4: the cache's codes go from HBM into the
+// operand tiles as they are, and the other operand is made to fit them.
+//   - A query head becomes two e4m3 terms that together hold its bf16 values
+//     (stage_q8), side by side as N = 2 x heads columns: one pass over the keys
+//     gives both partial logits, which are added in fp32.
+//   - A probability becomes two e5m2 terms, p ~ hi + lo, each added into the same
+//     accumulator: together they carry p to 2^-7 at worst and 0.24 % in the rms (bf16: 2^-8,
+//     0.16 %) over the 26 binades below the running maximum, so that a key
+//     which takes nearly all the probability does not flush the others.
+//   - The block scales are per key, and the keys lie on TMEM lanes (S^T = K Q^T,
+//     M = 128 keys): each thread owns one key and multiplies by its scale. With
+//     z the logits in log2 units, P' = 2^(z + e - M) is what multiplies the codes;
+//     the running maximum M is taken over z + e, and the softmax sum is that of
+//     P' 2^-e, so no other rescaling is needed.
+// The value product runs transposed as well, O^T = V^T P (M = 128 value columns,
+// N = heads): V^T is the key tile itself read MN-major, so each cached byte is
+// staged once and used by both products, and O of 64 heads takes 256 of the 512
+// TMEM columns of one SM. One CTA works on up to 64 heads; more heads are
+// spread over two CTAs that walk the same keys side by side (the second reads
+// them from L2).
+//
+// A small-N MMA is bound by its operand reads from shared memory (4 KB of keys +
+// N x 32 bytes, 128 bytes a cycle; measured 64, 48, 40 and 39 cycles for N = 128, 64,
+// 32, 16), so a tile of 128 keys takes 18 x 64 + 32 x 48 = 2690 cycles at 64 heads
+// and 18 x 40 + 32 x 39 = 1970 at 16. Against that stand 73.7 KB a tile from HBM: 3200
+// cycles at the device's 6.56 TB/s. So few heads are bound by HBM and 128 heads by
+// the tensor pipe (at 0.8 of what the bf16 rate would allow).
+//
+// Work split: the tiles of all queries in a row are cut into equal ranges, one
+// per CTA (per pair of CTAs above 64 heads), so ragged lengths, single queries
+// and large batches all fill the device. A query cut by a range end leaves
+// fp32 partial results that a second kernel joins.
+//
+// Roles: warps 0-7 softmax and epilogue (warp w: keys 32 (w & 3) .. of the tile,
+// one half of the heads each four), warp 8 MMA issue, warps 9-12 copies.
+#include "kv8_gather.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kSoftWarps = 8;
+constexpr int kMmaWarp = 8;
+constexpr int kThreads = 32 * (kSoftWarps + 1 + kGatherWarps);
+constexpr int kMaxWorkers = 148;
+// P' is kept within [0, 2^(kRescale + kShift)]: the maximum M is only moved when a
+// tile exceeds it by 2^kRescale, and P' is scaled by 2^kShift so that e5m2's
+// range (57344 = 1.75 * 2^15) is used to the top.
+constexpr float kRescale = 6.f;
+constexpr float kShift = 9.f;
+constexpr float kLn2 = 0.69314718055994531f;
 
-__global__ void __launch_bounds__(kWarps * 32)
-kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a) {
-  __shared__ float s_m[kWarps], s_l[kWarps];
-  __shared__ float s_o[kWarps][512];
-  const int qi = blockIdx.x, h = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int seq, pos;
-  if (!kv8_query(a.keys, qi, seq, pos) && threadIdx.x == 0 && h == 0)
-    report(a.status, DSA_ERR_DEVICE_BOUNDS);
-  const __nv_bfloat16* q = a.q + qi * a.ld_q + static_cast<int64_t>(h) * kRow8;
-  // lane owns columns 4 (lane + 32 i) .. +3 for i < 4 and rope columns 512 + 2 lane, +1
-  float qv[18];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) qv[4 * i + j] = __bfloat162float(q[4 * (lane + 32 * i) + j]);
-  qv[16] = __bfloat162float(q[512 + 2 * lane]);
-  qv[17] = __bfloat162float(q[513 + 2 * lane]);
-  float m = -INFINITY, l = 0.f, o[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = 0.f;
-  const int n = a.idx != nullptr ? a.k : pos + 1;
-  for (int j = warp; j < n; j += kWarps) {
-    const int p = a.idx != nullptr ? __ldg(a.idx + qi * a.ld_idx + j) : j;
-    if (p < 0) continue;
-    const int64_t row = p <= pos ? kv8_row(a.keys, seq, p) : -1;
-    if (row < 0) {
-      if (lane == 0) report(a.status, DSA_ERR_DEVICE_BOUNDS);
-      continue;
-    }
-    const uint8_t* kr = a.kv + row * a.ld_kv;
-    const float f = pow2i(a.exps[row >> 6]);
-    float v[18];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(kr) + lane + 32 * i);
-      const float2 x = from_e4m3x2(w & 0xffffu), y = from_e4m3x2(w >> 16);
-      v[4 * i] = x.x * f;
-      v[4 * i + 1] = x.y * f;
-      v[4 * i + 2] = y.x * f;
-      v[4 * i + 3] = y.y * f;
-    }
-    const float2 x = from_e4m3x2(__ldg(reinterpret_cast<const uint16_t*>(kr + 512) + lane));
-    v[16] = x.x * f;
-    v[17] = x.y * f;
-    float dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < 18; ++i) dot = fmaf(qv[i], v[i], dot);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
-    const float z = dot * a.scale_log2;
-    const float m_new = fmaxf(m, z);
-    const float alpha = exp2f(m - m_new), w = exp2f(z - m_new);
-    l = l * alpha + w;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = fmaf(o[i], alpha, w * v[i]);
-    m = m_new;
+template <int NP> struct Cfg {
+  static constexpr int kRing = NP == 64 ? 7 : 9;
+  static constexpr uint32_t kTmem = NP == 64 ? 512 : NP == 32 ? 256 : 128;
+  static constexpr uint32_t kColS = 4 * NP;          // two buffers of 2 NP columns
+};
+
+template <int NP>
+struct __align__(1024) Smem {
+  Kv8Ring<Cfg<NP>::kRing> ring;
+  alignas(1024) uint8_t q[2 * NP * 576];
+  alignas(1024) uint8_t p[kTile * 128];              // row = key: first terms at byte 0, second at 64
+  alignas(16) float head_scale[2][NP];               // logit2 = (hi + lo / 16) * 2^e * head_scale
+  alignas(16) float ref[kSoftWarps][NP / 2];         // M - kShift, a copy per warp
+  alignas(16) float alpha[kSoftWarps][NP / 2];
+  float tile_max[2][4][NP];
+  float sum[4][NP];
+  int64_t scratch[kThreads / 32 + 2];
+  uint64_t q_full, p_full, pv_done, drained;
+  uint64_t s_full[2], s_empty[2];
+  uint32_t tmem_base;
+};
+
+// Workspace: which query each worker's first and last range end cuts, then the
+// partial results of slots 2 w (first) and 2 w + 1 (last).
+struct Partials {
+  int32_t* head_item;       // [workers] query cut by the worker's beginning, or -1
+  int32_t* head_goes_on;    // [workers] 1: that query is cut by its end as well
+  int32_t* tail_item;       // [workers] query that begins here and is cut by the end, or -1
+  float2* ml;               // [2 workers][heads] running maximum, sum
+  float* o;                 // [2 workers][heads][512]
+};
+
+__host__ __device__ inline size_t partials_bytes(int workers, int heads) {
+  return 2048 + static_cast<size_t>(2) * workers * heads * (sizeof(float2) + 512 * sizeof(float));
+}
+
+__host__ __device__ inline Partials partials(void* ws, int workers, int heads) {
+  Partials p;
+  p.head_item = static_cast<int32_t*>(ws);
+  p.head_goes_on = p.head_item + kMaxWorkers;
+  p.tail_item = p.head_goes_on + kMaxWorkers;
+  p.o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 2048);
+  p.ml = reinterpret_cast<float2*>(p.o + static_cast<size_t>(2) * workers * heads * 512);
+  return p;
+}
+static_assert(3 * kMaxWorkers * sizeof(int32_t) <= 2048, "");
+
+// One query's part of a worker's range.
+struct Piece {
+  int qi, j0, n, tiles;     // tiles [j0, j0 + n) of the query's `tiles`
+};
+
+struct Pieces {
+  const Kv8AttnArgs& a;
+  int64_t left;
+  int qi, j0;
+  __device__ Pieces(const Kv8AttnArgs& args, const Kv8Range& r)
+      : a(args), left(r.t1 - r.t0), qi(r.qi), j0(r.j0) {}
+  __device__ __forceinline__ bool next(Piece& p) {
+    if (left <= 0) return false;
+    p.qi = qi;
+    p.j0 = j0;
+    p.tiles = kv8_tiles(a.keys, a.idx != nullptr, a.k, qi);
+    p.n = static_cast<int>(min(left, static_cast<int64_t>(p.tiles - j0)));
+    left -= p.n;
+    ++qi;
+    j0 = 0;
+    return true;
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s_o[warp][4 * (lane + 32 * i) + j] = o[4 * i + j];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
+};
+
+template <int NP>
+__global__ void __launch_bounds__(kThreads, 1)
+kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_heads, int workers) {
+  constexpr int R = Cfg<NP>::kRing;
+  constexpr int HN = NP / 2;                         // heads of a softmax warp
+  extern __shared__ uint8_t smem_raw[];
+  Smem<NP>& S = *reinterpret_cast<Smem<NP>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const int warp = warp_id(), lane = threadIdx.x & 31;
+  const int worker = blockIdx.x / groups, group = blockIdx.x % groups;
+  const int head0 = group * group_heads;
+  const int live = min(group_heads, a.heads - head0);
+  const Partials part = partials(a.ws, workers, a.heads);
+
+  const Kv8Range range = kv8_range<kThreads>(a.keys, a.idx != nullptr, a.k, worker, workers, S.scratch);
+  if (threadIdx.x == 0 && group == 0) part.head_item[worker] = part.tail_item[worker] = -1;
+  if (range.t0 == range.t1) return;
+  if (threadIdx.x == 0) {
+    S.ring.init();
+    mbar_init(&S.q_full, kSoftWarps);
+    mbar_init(&S.p_full, kSoftWarps);
+    mbar_init(&S.pv_done, 1);
+    mbar_init(&S.drained, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&S.s_full[b], 1);
+      mbar_init(&S.s_empty[b], kSoftWarps);
+    }
+    fence_barrier_init();
   }
+  if (warp == kMmaWarp) tmem_alloc(&S.tmem_base, Cfg<NP>::kTmem);
+  tc_fence_before();
   __syncthreads();
-  float mx = -INFINITY, sum = 0.f;
-  for (int w = 0; w < kWarps; ++w)
-    if (s_l[w] != 0.f) mx = fmaxf(mx, s_m[w]);
-  float part[kWarps];
-  for (int w = 0; w < kWarps; ++w) {
-    part[w] = s_l[w] != 0.f ? exp2f(s_m[w] - mx) : 0.f;
-    sum += part[w] * s_l[w];
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  Pieces pieces(a, range);
+  Piece pc;
+
+  if (warp > kMmaWarp) {
+    // ------------------------------------------------------------ copies
+    Kv8Gather<R> g{S.ring, a, lane, warp - kMmaWarp - 1};
+    while (pieces.next(pc))
+      if (!g.run(pc.qi, pc.j0, pc.n)) break;
+    g.drain();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue
+    // Per tile: S^T(g) over chunks 0-2 and the rope columns; O^T += V^T P of the
+    // tile before over chunk 0, which frees the slot that chunk 3 of tile g may
+    // still wait for; chunk 3; the rest of the tile before. The softmax of tile g
+    // then has the value products of g - 1 and the logits of g + 1 to hide behind.
+    constexpr uint32_t idesc_qk = make_idesc(2 * NP, 0, 0, 0, 0);
+    constexpr uint32_t idesc_pv = make_idesc(NP, 0, 1, 1, 1);   // e4m3 codes, e5m2 probabilities
+    const uint64_t q_desc = sw128_desc(smem_u32(S.q), 16, 1024);
+    const uint64_t qr_desc = sw64_desc(smem_u32(S.q) + 4 * (2 * NP * 128));
+    const uint64_t p_desc = sw128_desc(smem_u32(S.p), 16384, 1024);
+    const uint64_t k_desc = sw128_desc(smem_u32(S.ring.chunk[0]), 16384, 1024);
+    const uint64_t r_desc = sw64_desc(smem_u32(S.ring.rope[0]));
+    uint32_t g = 0;                                  // tiles begun
+    uint32_t ck = 0, cv = 0;                         // chunks taken by the logits, by the values
+    uint32_t n_piece = 0;
+    bool ok = true;
+
+    auto qk_chunk = [&](int c) -> bool {
+      const uint32_t slot = ck % R;
+      if (!mbar_wait_warp(&S.ring.full[slot], (ck / R) & 1, a.status)) return false;
+      tc_fence_after();
+      const uint64_t kd = k_desc + slot * (kChunkB / 16), qd = q_desc + c * (2 * NP * 128 / 16);
+      const uint32_t d = tmem + Cfg<NP>::kColS + (g & 1) * (2 * NP);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_f8(d, kd + 2 * k, qd + 2 * k, idesc_qk, c > 0 || k > 0);
+      }
+      __syncwarp();
+      ++ck;
+      return true;
+    };
+    auto pv_chunk = [&](int c, bool first) {
+      const uint32_t slot = cv % R;
+      const uint64_t vd = k_desc + slot * (kChunkB / 16);
+      const uint32_t d = tmem + c * NP;
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          mma_f8(d, vd + 256 * k, p_desc + 256 * k, idesc_pv, !first || k > 0);
+          mma_f8(d, vd + 256 * k, p_desc + 256 * k + 4, idesc_pv, 1);
+        }
+        mma_commit(&S.ring.empty[slot]);
+        if (c == 3) mma_commit(&S.pv_done);
+      }
+      __syncwarp();
+      ++cv;
+    };
+    auto p_ready = [&](uint32_t tile) -> bool {
+      if (!mbar_wait_warp(&S.p_full, tile & 1, a.status)) return false;
+      tc_fence_after();
+      return true;
+    };
+
+    while (ok && pieces.next(pc)) {
+      ok = mbar_wait_warp(&S.q_full, n_piece & 1, a.status);
+      ++n_piece;
+      for (int j = 0; j < pc.n && ok; ++j) {
+        ok = mbar_wait_warp(&S.s_empty[g & 1], ((g >> 1) & 1) ^ 1, a.status);
+        for (int c = 0; c < 3 && ok; ++c) ok = qk_chunk(c);
+        if (!ok) break;
+        const uint32_t rs = g % kRopeRing;
+        ok = mbar_wait_warp(&S.ring.rope_full[rs], (g / kRopeRing) & 1, a.status);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t d = tmem + Cfg<NP>::kColS + (g & 1) * (2 * NP);
+          const uint64_t rd = r_desc + rs * (kRopeB / 16);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) mma_f8(d, rd + 2 * k, qr_desc + 2 * k, idesc_qk, 1);
+          mma_commit(&S.ring.rope_empty[rs]);
+        }
+        __syncwarp();
+        if (j > 0) {
+          ok = p_ready(g - 1);
+          if (!ok) break;
+          pv_chunk(0, j == 1);
+        }
+        ok = qk_chunk(3);
+        if (!ok) break;
+        if (elect_one()) mma_commit(&S.s_full[g & 1]);
+        __syncwarp();
+        if (j > 0)
+          for (int c = 1; c < 4; ++c) pv_chunk(c, j == 1);
+        ++g;
+      }
+      if (ok) ok = p_ready(g - 1);
+      if (ok)
+        for (int c = 0; c < 4; ++c) pv_chunk(c, pc.n == 1);
+    }
+    // nothing is in flight when the block ends, whichever way it got here
+    if (elect_one()) mma_commit(&S.drained);
+    __syncwarp();
+    mbar_wait_warp(&S.drained, 0, a.status);
+  } else {
+    // ------------------------------------------------------------ softmax and epilogue
+    const int sub = warp & 3, half = warp >> 2;
+    const int key = 32 * sub + lane;                 // this thread's key of each tile
+    const int hb = half * HN;                        // first head of this warp's half
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * sub) << 16);
+    const uint32_t s_col = Cfg<NP>::kColS + hb;
+    uint8_t* const p_row = S.p + key * 128;
+    const uint32_t sw = key & 7;
+    const uint32_t bar = 1 + half;                   // the four warps of a half
+    uint32_t g = 0, n_piece = 0;
+    bool ok = true;
+    bool more = pieces.next(pc);
+
+    auto stage_q = [&](const Piece& p, uint32_t n) {
+      const __nv_bfloat16* q = a.q + static_cast<int64_t>(p.qi) * a.ld_q +
+                               static_cast<int64_t>(head0) * kRow8;
+      stage_q8<NP>(S.q, q, live, warp, kSoftWarps, lane, [&](int h, int s) {
+        S.head_scale[n & 1][h] = a.scale_log2 * pow2i(s);
+      });
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.q_full);
+      named_bar_sync(3, 32 * kSoftWarps);            // head_scale is complete
+    };
+    stage_q(pc, 0);
+
+    while (more && ok) {
+      const float* const hs = S.head_scale[n_piece & 1] + hb;
+      float m_used = -INFINITY;                      // lane h < HN: running maximum of head hb + h
+      float l[HN];
+#pragma unroll
+      for (int i = 0; i < HN; ++i) l[i] = 0.f;
+      for (int j = 0; j < pc.n; ++j, ++g) {
+        const uint32_t b = g & 1;
+        if (!mbar_wait_warp(&S.ring.meta_full[g % kMetaRing], (g / kMetaRing) & 1, a.status) ||
+            !mbar_wait_warp(&S.s_full[b], (g >> 1) & 1, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float ks = S.ring.key_scale[g % kMetaRing][key];
+        const bool valid = ks > 0.f;
+        const float e_key = static_cast<float>(static_cast<int>(__float_as_uint(ks) >> 23) - 127);
+        float y[HN];
+        {
+          uint32_t v[HN], w[HN];
+          tmem_ld<HN>(t_lane + s_col + b * (2 * NP), v);
+          tmem_ld<HN>(t_lane + s_col + b * (2 * NP) + NP, w);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.s_empty[b]);
+          const float4* h4 = reinterpret_cast<const float4*>(hs);
+#pragma unroll
+          for (int i = 0; i < HN; i += 4) {
+            const float4 f = h4[i / 4];
+            const float ff[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const float s = fmaf(__uint_as_float(w[i + t]), 0.0625f, __uint_as_float(v[i + t])) * ks;
+              y[i + t] = valid ? fmaf(s, ff[t], e_key) : -INFINITY;
+            }
+          }
+        }
+        // maximum of each head over the tile's 128 keys
+        float mine = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < HN; ++i) {
+          const float m = warp_max(y[i]);
+          if (lane == i) mine = m;
+        }
+        if (lane < HN) S.tile_max[b][sub][hb + lane] = mine;
+        named_bar_sync(bar, 128);
+        float mx = -INFINITY;
+        if (lane < HN)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) mx = fmaxf(mx, S.tile_max[b][w][hb + lane]);
+        const bool move = mx > m_used + kRescale;    // (true for the first key: m_used = -inf)
+        const float m_next = move ? mx : m_used;
+        const float alpha = move ? ex2(m_used - m_next) : 1.f;
+        m_used = m_next;
+        if (lane < HN) {
+          S.ref[warp][lane] = m_next == -INFINITY ? 0.f : m_next - kShift;
+          S.alpha[warp][lane] = alpha;
+        }
+        __syncwarp();
+        const bool rescale = __any_sync(0xffffffffu, move && lane < HN) && j > 0;
+        if (rescale) {
+          const float4* a4 = reinterpret_cast<const float4*>(S.alpha[warp]);
+#pragma unroll
+          for (int i = 0; i < HN; i += 4) {
+            const float4 f = a4[i / 4];
+            l[i] *= f.x;
+            l[i + 1] *= f.y;
+            l[i + 2] *= f.z;
+            l[i + 3] *= f.w;
+          }
+        }
+        // P' and its two terms
+        uint32_t hi[HN / 4], lo[HN / 4];
+        const float inv_scale = valid ? pow2i(-static_cast<int>(e_key)) : 0.f;
+        const float4* r4 = reinterpret_cast<const float4*>(S.ref[warp]);
+#pragma unroll
+        for (int i = 0; i < HN; i += 4) {
+          const float4 r = r4[i / 4];
+          const float p0 = ex2(y[i] - r.x), p1 = ex2(y[i + 1] - r.y);
+          const float p2 = ex2(y[i + 2] - r.z), p3 = ex2(y[i + 3] - r.w);
+          l[i] = fmaf(p0, inv_scale, l[i]);
+          l[i + 1] = fmaf(p1, inv_scale, l[i + 1]);
+          l[i + 2] = fmaf(p2, inv_scale, l[i + 2]);
+          l[i + 3] = fmaf(p3, inv_scale, l[i + 3]);
+          const uint32_t h0 = to_e5m2x2(p0, p1), h1 = to_e5m2x2(p2, p3);
+          const float2 b0 = from_e5m2x2(h0), b1 = from_e5m2x2(h1);
+          hi[i / 4] = h0 | (h1 << 16);
+          lo[i / 4] = to_e5m2x2(p0 - b0.x, p1 - b0.y) | (to_e5m2x2(p2 - b1.x, p3 - b1.y) << 16);
+        }
+        // the value products of the tile before are done: P and O may be written
+        if (g > 0 && !mbar_wait_warp(&S.pv_done, (g - 1) & 1, a.status)) {
+          ok = false;
+          break;
+        }
+        if (rescale) {
+          tc_fence_after();
+          const float4* a4 = reinterpret_cast<const float4*>(S.alpha[warp]);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < HN; i += 8) {
+              uint32_t o[8];
+              tmem_ld8(t_lane + c * NP + hb + i, o);
+              tmem_wait_ld();
+              const float4 f0 = a4[i / 4], f1 = a4[i / 4 + 1];
+              const float ff[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+              for (int t = 0; t < 8; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * ff[t]);
+              tmem_st8(t_lane + c * NP + hb + i, o);
+            }
+          tmem_wait_st();
+        }
+        if constexpr (HN == 8) {
+          const uint32_t at = ((0 ^ sw) << 4) + hb, at2 = ((4 ^ sw) << 4) + hb;
+          *reinterpret_cast<uint2*>(p_row + at) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(p_row + at2) = make_uint2(lo[0], lo[1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < HN / 16; ++i) {
+            const uint32_t c = hb / 16 + i;
+            *reinterpret_cast<uint4*>(p_row + ((c ^ sw) << 4)) =
+                make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+            *reinterpret_cast<uint4*>(p_row + (((c + 4) ^ sw) << 4)) =
+                make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_full);
+      }
+      if (!ok) break;
+      // the next query's logits may start while this one's result is written out
+      const Piece done = pc;
+      more = pieces.next(pc);
+      if (more) stage_q(pc, n_piece + 1);
+      ++n_piece;
+
+      // sums over the keys: lanes, then the four warps in order
+      const float lw = reduce_columns<HN>(l, lane);
+      if (lane < HN) S.sum[sub][hb + lane] = lw;
+      named_bar_sync(bar, 128);
+      const bool cut = done.n < done.tiles;
+      const int slot = 2 * worker + (done.j0 == 0 ? 1 : 0);
+      if (lane < HN) {
+        const float lt = ((S.sum[0][hb + lane] + S.sum[1][hb + lane]) + S.sum[2][hb + lane]) +
+                         S.sum[3][hb + lane];
+        const float ref = m_used == -INFINITY ? 0.f : m_used - kShift;
+        S.alpha[warp][lane] = lt == 0.f ? 0.f : 1.f / lt;
+        if (sub == 0 && hb + lane < live) {
+          const int64_t h = head0 + hb + lane;
+          if (cut)
+            part.ml[static_cast<int64_t>(slot) * a.heads + h] = make_float2(ref, lt);
+          else if (a.lse != nullptr)
+            a.lse[static_cast<int64_t>(done.qi) * a.heads + h] =
+                lt == 0.f ? -INFINITY : (ref + log2f(lt)) * kLn2;
+        }
+      }
+      __syncwarp();
+      if (!mbar_wait_warp(&S.pv_done, (g - 1) & 1, a.status)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      // O^T: lane = value column, TMEM column = head
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        const int dim = c * 128 + 32 * sub + lane;
+#pragma unroll 1
+        for (int i = 0; i < HN; i += 8) {
+          uint32_t o[8];
+          tmem_ld8(t_lane + c * NP + hb + i, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            if (hb + i + t >= live) break;
+            const int64_t h = head0 + hb + i + t;
+            const float v = __uint_as_float(o[t]);
+            if (cut)
+              part.o[(static_cast<int64_t>(slot) * a.heads + h) * 512 + dim] = v;
+            else
+              a.out[(static_cast<int64_t>(done.qi) * a.heads + h) * 512 + dim] =
+                  __float2bfloat16(S.alpha[warp][i + t] == 0.f ? 0.f : v * S.alpha[warp][i + t]);
+          }
+        }
+      }
+      tc_fence_before();
+      if (threadIdx.x == 0 && group == 0) {
+        if (cut && done.j0 > 0) {
+          part.head_item[worker] = done.qi;
+          part.head_goes_on[worker] = done.j0 + done.n < done.tiles;
+        } else if (cut) {
+          part.tail_item[worker] = done.qi;
+        }
+      }
+    }
   }
-  const int64_t at = static_cast<int64_t>(qi) * a.heads + h;
-  for (int d = threadIdx.x; d < 512; d += kWarps * 32) {
-    float r = 0.f;
-    for (int w = 0; w < kWarps; ++w) r = fmaf(part[w], s_o[w][d], r);
-    a.out[at * 512 + d] = __float2bfloat16(sum != 0.f ? r / sum : 0.f);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg<NP>::kTmem);
   }
-  if (threadIdx.x == 0 && a.lse != nullptr)
-    a.lse[at] = sum != 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Joins the pieces of each query that a range end cut. Block (w, h): the query
+// that begins in worker w's range and goes on, head h.
+__global__ void __launch_bounds__(128)
+kv8_join_kernel(const __grid_constant__ Kv8AttnArgs a, int workers) {
+  griddep_wait();
+  const Partials part = partials(a.ws, workers, a.heads);
+  const int w = blockIdx.x, h = blockIdx.y;
+  const int qi = part.tail_item[w];
+  if (qi < 0) return;
+  // its pieces: the last of worker w, then the first of the next workers that
+  // have any tiles, up to the one that does not go on
+  float m = -INFINITY;
+  int last = workers - 1;
+  for (int i = w; i <= last; ++i) {
+    if (i > w && part.head_item[i] != qi) continue;
+    const float2 ml = part.ml[static_cast<int64_t>(2 * i + (i == w ? 1 : 0)) * a.heads + h];
+    if (ml.y != 0.f) m = fmaxf(m, ml.x);
+    if (i > w && part.head_goes_on[i] == 0) last = i;
+  }
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = w; i <= last; ++i) {
+    if (i > w && part.head_item[i] != qi) continue;
+    const int64_t at = static_cast<int64_t>(2 * i + (i == w ? 1 : 0)) * a.heads + h;
+    const float2 ml = part.ml[at];
+    if (ml.y == 0.f) continue;                       // no key of this piece counts
+    const float f = exp2f(ml.x - m);
+    const float4 v = reinterpret_cast<const float4*>(part.o + at * 512)[threadIdx.x];
+    l = fmaf(ml.y, f, l);
+    o.x = fmaf(v.x, f, o.x);
+    o.y = fmaf(v.y, f, o.y);
+    o.z = fmaf(v.z, f, o.z);
+    o.w = fmaf(v.w, f, o.w);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t out = static_cast<int64_t>(qi) * a.heads + h;
+  const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+  const __nv_bfloat162 y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  reinterpret_cast<uint2*>(a.out + out * 512)[threadIdx.x] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  if (threadIdx.x == 0 && a.lse != nullptr) a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+struct Split {
+  int groups, group_heads, workers;
+};
+
+// Head groups of at most 64, and as many workers as the device holds, but no
+// more than there can be tiles.
+Split split(int32_t n_q, int32_t heads, int64_t max_keys, int num_sms) {
+  Split s;
+  s.groups = (heads + 63) / 64;
+  s.group_heads = (heads + s.groups - 1) / s.groups;
+  const int64_t tiles = n_q * ((max_keys + kTile - 1) / kTile);
+  const int64_t most = (num_sms < kMaxWorkers ? num_sms : kMaxWorkers) / s.groups;
+  s.workers = static_cast<int>(tiles < most ? tiles : most);
+  return s;
+}
+
+template <int NP>
+cudaError_t launch(const Kv8AttnArgs& a, const Split& s, cudaStream_t stream) {
+  const size_t smem = sizeof(Smem<NP>) + 1024;
+  static_assert(sizeof(Smem<NP>) + 1024 <= 232448, "shared memory of one SM");
+  cudaError_t e = cudaFuncSetAttribute(kv8_mqa_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  kv8_mqa_kernel<NP><<<s.workers * s.groups, kThreads, smem, stream>>>(a, s.groups, s.group_heads, s.workers);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t kv8_mqa_workspace(int32_t, int32_t, int64_t) { return 0; }
+size_t kv8_mqa_workspace(int32_t n_q, int32_t heads, int64_t max_keys) {
+  const Split s = split(n_q, heads, max_keys, kMaxWorkers);
+  return (partials_bytes(s.workers, heads) + 255) & ~size_t(255);
+}
 
-cudaError_t launch_kv8_mqa(const Kv8AttnArgs& a, int, int* launches, cudaStream_t stream) {
-  kv8_mqa_kernel<<<dim3(a.keys.n_q, a.heads), kWarps * 32, 0, stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) ++*launches;
-  return e;
+cudaError_t launch_kv8_mqa(const Kv8AttnArgs& a, int num_sms, int* launches, cudaStream_t stream) {
+  const int64_t max_keys = a.idx != nullptr ? a.k
+                           : a.keys.paged   ? static_cast<int64_t>(a.keys.max_pages) * 64
+                                            : a.keys.n_keys;
+  const Split s = split(a.keys.n_q, a.heads, max_keys, num_sms);
+  cudaError_t e = s.group_heads <= 16   ? launch<16>(a, s, stream)
+                  : s.group_heads <= 32 ? launch<32>(a, s, stream)
+                                        : launch<64>(a, s, stream);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(s.workers, a.heads);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv8_join_kernel, a, s.workers);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  return cudaSuccess;
 }
 
 }  // namespace dsa
