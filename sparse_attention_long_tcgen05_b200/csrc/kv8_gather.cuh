@@ -11,7 +11,12 @@ constexpr int kChunkB = kTile * 128; // 128 columns of a tile's keys: 16 KB
 constexpr int kRopeB = kTile * 64;   // the 64 rope columns: 8 KB
 constexpr int kRopeRing = 2;
 constexpr int kMetaRing = 4;
-constexpr int kInFlight = 4;         // copy groups of a warp that may be pending after an issue
+
+// Arrives on `bar` (one of its expected arrivals) when all copies that this
+// thread has issued have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 // The ring of a kernel: R chunk slots, two rope slots, and the scale of each
 // key of a tile (2^e, or 0 for a key that does not count).
@@ -26,11 +31,11 @@ struct __align__(1024) Kv8Ring {
 
   __device__ void init() {
     for (int i = 0; i < R; ++i) {
-      mbar_init(&full[i], kGatherWarps);
+      mbar_init(&full[i], 32 * kGatherWarps);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kRopeRing; ++i) {
-      mbar_init(&rope_full[i], kGatherWarps);
+      mbar_init(&rope_full[i], 32 * kGatherWarps);
       mbar_init(&rope_empty[i], 1);
     }
     for (int i = 0; i < kMetaRing; ++i) mbar_init(&meta_full[i], kGatherWarps);
@@ -38,54 +43,19 @@ struct __align__(1024) Kv8Ring {
 };
 
 // One copying warp. Units of a tile in the order in which the MMAs want them:
-// chunks 0, 1, 2, rope, chunk 3. A unit is released to the MMA issuer once this
-// warp's copies of it have landed, at the latest when kInFlight newer ones have
-// been issued, and always before the warp waits for a slot: the issuer frees
-// slots in order, so nothing that it needs may be held back here.
+// chunks 0, 1, 2, rope, chunk 3. Every lane's arrival on a unit's barrier is
+// made by the copy engine when that lane's copies have landed
+// (cp.async.mbarrier.arrive.noinc), so a warp only ever waits for free slots and
+// runs as far ahead as the ring allows; the MMA issuer, having waited, makes the
+// copied bytes visible to the tensor core with a proxy fence of its own. (With
+// the fence on this side a warp first had to wait for its copies, and the fence
+// also waits for the newer ones: a unit took ~8000 cycles instead.)
 template <int R>
 struct Kv8Gather {
   Kv8Ring<R>& ring;
   const Kv8AttnArgs& a;
   int lane, g;             // g: copying warp 0..3
-  uint32_t issued = 0, released = 0;      // units
   uint32_t n_chunk = 0, n_rope = 0, n_tile = 0;
-  uint32_t rel_chunk = 0, rel_rope = 0;
-
-  __device__ __forceinline__ void release_oldest() {
-    switch (issued - released) {
-      case 1: cp_async_wait_group<0>(); break;
-      case 2: cp_async_wait_group<1>(); break;
-      case 3: cp_async_wait_group<2>(); break;
-      case 4: cp_async_wait_group<3>(); break;
-      default: cp_async_wait_group<4>(); break;
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (released % 5 == 3) {
-      if (lane == 0) mbar_arrive(&ring.rope_full[rel_rope % kRopeRing]);
-      ++rel_rope;
-    } else {
-      if (lane == 0) mbar_arrive(&ring.full[rel_chunk % R]);
-      ++rel_chunk;
-    }
-    ++released;
-  }
-
-  // Waits until `bar` has completed the phase of `parity`, releasing what is
-  // pending first.
-  __device__ __forceinline__ bool wait_slot(uint64_t* bar, uint32_t parity) {
-    while (issued != released) {
-      if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity, 1))) return true;
-      release_oldest();
-    }
-    return mbar_wait_warp(bar, parity, a.status);
-  }
-
-  __device__ __forceinline__ void committed() {
-    cp_async_commit();
-    ++issued;
-    if (issued - released > kInFlight) release_oldest();
-  }
 
   // Key position of this lane's row in tile j of query qi: p in [0, pos], or -1;
   // bad: an entry past the query's position.
@@ -127,7 +97,8 @@ struct Kv8Gather {
       for (int u = 0; u < 5; ++u) {
         if (u == 3) {
           const uint32_t slot = n_rope % kRopeRing;
-          if (!wait_slot(&ring.rope_empty[slot], ((n_rope / kRopeRing) & 1) ^ 1)) return false;
+          if (!mbar_wait_warp(&ring.rope_empty[slot], ((n_rope / kRopeRing) & 1) ^ 1, a.status))
+            return false;
           const uint32_t dst = smem_u32(ring.rope[slot]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -137,11 +108,12 @@ struct Kv8Gather {
             cp_async16_or_zero(dst + r * 64 + ((((lane & 3) ^ (r >> 1)) & 3) << 4),
                                reinterpret_cast<const void*>(s), (ok_mask >> rr) & 1u);
           }
+          cp_async_arrive(&ring.rope_full[slot]);
           ++n_rope;
         } else {
           const int c = u < 3 ? u : 3;
           const uint32_t slot = n_chunk % R;
-          if (!wait_slot(&ring.empty[slot], ((n_chunk / R) & 1) ^ 1)) return false;
+          if (!mbar_wait_warp(&ring.empty[slot], ((n_chunk / R) & 1) ^ 1, a.status)) return false;
           if (u == 0) {
             // the scales: slot n_tile % 4 was read long ago (chunk slots of the
             // tile before last are only free after its softmax)
@@ -159,9 +131,9 @@ struct Kv8Gather {
             cp_async16_or_zero(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
                                reinterpret_cast<const void*>(at[i] + 128 * c), (ok_mask >> rr) & 1u);
           }
+          cp_async_arrive(&ring.full[slot]);
           ++n_chunk;
         }
-        committed();
         if (u == 1 && p_next >= 0) row_next = kv8_row(a.keys, seq, p_next);
       }
       p = p_next;
@@ -172,8 +144,9 @@ struct Kv8Gather {
     return true;
   }
 
+  // No copy is in flight when the block ends.
   __device__ __forceinline__ void drain() {
-    while (issued != released) release_oldest();
+    cp_async_commit();
     cp_async_wait_group<0>();
   }
 };

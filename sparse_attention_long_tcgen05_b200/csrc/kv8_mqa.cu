@@ -190,6 +190,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
     auto qk_chunk = [&](int c) -> bool {
       const uint32_t slot = ck % R;
       if (!mbar_wait_warp(&S.ring.full[slot], (ck / R) & 1, a.status)) return false;
+      fence_proxy_async_smem();                      // the copies, before the MMAs read them
       tc_fence_after();
       const uint64_t kd = k_desc + slot * (kChunkB / 16), qd = q_desc + c * (2 * NP * 128 / 16);
       const uint32_t d = tmem + Cfg<NP>::kColS + (g & 1) * (2 * NP);
@@ -233,6 +234,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
         const uint32_t rs = g % kRopeRing;
         ok = mbar_wait_warp(&S.ring.rope_full[rs], (g / kRopeRing) & 1, a.status);
         if (!ok) break;
+        fence_proxy_async_smem();
         tc_fence_after();
         if (elect_one()) {
           const uint32_t d = tmem + Cfg<NP>::kColS + (g & 1) * (2 * NP);
