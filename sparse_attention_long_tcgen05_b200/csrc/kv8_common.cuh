@@ -64,6 +64,20 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Whether the phase with the given parity has completed, without waiting at all
+// (try_wait suspends the warp for microseconds, whatever hint it is given).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+
 // Descriptor of a K-major tile with 64-byte rows, 64-byte swizzle (512-byte
 // aligned base; 8-row groups 512 bytes apart).
 __device__ __forceinline__ uint64_t sw64_desc(uint32_t smem_addr) {

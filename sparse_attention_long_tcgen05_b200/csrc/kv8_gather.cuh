@@ -9,8 +9,7 @@ namespace dsa {
 constexpr int kGatherWarps = 4;      // warp g copies keys 32 g .. 32 g + 31 of a tile
 constexpr int kChunkB = kTile * 128; // 128 columns of a tile's keys: 16 KB
 constexpr int kRopeB = kTile * 64;   // the 64 rope columns: 8 KB
-constexpr int kRopeRing = 2;
-constexpr int kMetaRing = 4;
+constexpr int8_t kNoKey = -128;      // key_exp of a key that does not count
 
 // Arrives on `bar` (one of its expected arrivals) when all copies that this
 // thread has issued have landed.
@@ -18,41 +17,47 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// The ring of a kernel: R chunk slots, two rope slots, and the scale of each
-// key of a tile (2^e, or 0 for a key that does not count).
+// The ring of a kernel: R chunk slots, one slot for the rope columns, and the
+// exponent of each key of a tile. A kernel whose chunk slots are freed by the
+// value products, after the tile's softmax, needs META = 2 exponent slots for R <=
+// 8 (slot 4 n of the chunk order waits for chunk 4 n - 8 of tile n - 2) and 4 for
+// R <= 12.
 template <int R>
-struct __align__(1024) Kv8Ring {
-  uint8_t chunk[R][kChunkB];
-  uint8_t rope[kRopeRing][kRopeB];
-  float key_scale[kMetaRing][kTile];
+struct Kv8Slots {
+  alignas(1024) uint8_t chunk[R][kChunkB];
+  alignas(1024) uint8_t rope[kRopeB];
+};
+
+template <int R, int META>
+struct Kv8Ring {
+  static constexpr int kSlots = R, kMeta = META;
+  int8_t key_exp[META][kTile];
   uint64_t full[R], empty[R];
-  uint64_t rope_full[kRopeRing], rope_empty[kRopeRing];
-  uint64_t meta_full[kMetaRing];
+  uint64_t rope_full, rope_empty;
+  uint64_t meta_full[META];
 
   __device__ void init() {
     for (int i = 0; i < R; ++i) {
       mbar_init(&full[i], 32 * kGatherWarps);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < kRopeRing; ++i) {
-      mbar_init(&rope_full[i], 32 * kGatherWarps);
-      mbar_init(&rope_empty[i], 1);
-    }
-    for (int i = 0; i < kMetaRing; ++i) mbar_init(&meta_full[i], kGatherWarps);
+    mbar_init(&rope_full, 32 * kGatherWarps);
+    mbar_init(&rope_empty, 1);
+    for (int i = 0; i < META; ++i) mbar_init(&meta_full[i], kGatherWarps);
   }
 };
 
 // One copying warp. Units of a tile in the order in which the MMAs want them:
-// chunks 0, 1, 2, rope, chunk 3. Every lane's arrival on a unit's barrier is
+// chunks 0, 1, 2, 3, then the rope columns. Every lane's arrival on a unit's barrier is
 // made by the copy engine when that lane's copies have landed
 // (cp.async.mbarrier.arrive.noinc), so a warp only ever waits for free slots and
 // runs as far ahead as the ring allows; the MMA issuer, having waited, makes the
-// copied bytes visible to the tensor core with a proxy fence of its own. (With
-// the fence on this side a warp first had to wait for its copies, and the fence
-// also waits for the newer ones: a unit took ~8000 cycles instead.)
-template <int R>
+// copied bytes visible to the tensor core with a proxy fence of its own.
+template <typename Ring>
 struct Kv8Gather {
-  Kv8Ring<R>& ring;
+  static constexpr int R = Ring::kSlots, kMeta = Ring::kMeta;
+  Ring& ring;
+  Kv8Slots<R>& slots;
   const Kv8AttnArgs& a;
   int lane, g;             // g: copying warp 0..3
   uint32_t n_chunk = 0, n_rope = 0, n_tile = 0;
@@ -83,8 +88,7 @@ struct Kv8Gather {
       if (p >= 0 && row < 0) any_bad = true;      // a page id out of range
       const bool ok = row >= 0;
       const uint8_t* src = a.kv + (ok ? row * a.ld_kv : 0);
-      float scale = 0.f;
-      if (ok) scale = pow2i(__ldg(a.exps + (row >> 6)));
+      const int8_t e = ok ? __ldg(a.exps + (row >> 6)) : kNoKey;
       const uint64_t src_bits = reinterpret_cast<uint64_t>(src);
       const uint32_t ok_mask = __ballot_sync(0xffffffffu, ok);
       // chunk copies: instruction i covers rows 4 i .. 4 i + 3 of this warp's 32
@@ -95,11 +99,9 @@ struct Kv8Gather {
       int64_t row_next = -1;
 #pragma unroll
       for (int u = 0; u < 5; ++u) {
-        if (u == 3) {
-          const uint32_t slot = n_rope % kRopeRing;
-          if (!mbar_wait_warp(&ring.rope_empty[slot], ((n_rope / kRopeRing) & 1) ^ 1, a.status))
-            return false;
-          const uint32_t dst = smem_u32(ring.rope[slot]);
+        if (u == 4) {
+          if (!mbar_wait_warp(&ring.rope_empty, (n_rope & 1) ^ 1, a.status)) return false;
+          const uint32_t dst = smem_u32(slots.rope);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int rr = 8 * i + (lane >> 2);
@@ -108,28 +110,25 @@ struct Kv8Gather {
             cp_async16_or_zero(dst + r * 64 + ((((lane & 3) ^ (r >> 1)) & 3) << 4),
                                reinterpret_cast<const void*>(s), (ok_mask >> rr) & 1u);
           }
-          cp_async_arrive(&ring.rope_full[slot]);
+          cp_async_arrive(&ring.rope_full);
           ++n_rope;
         } else {
-          const int c = u < 3 ? u : 3;
           const uint32_t slot = n_chunk % R;
           if (!mbar_wait_warp(&ring.empty[slot], ((n_chunk / R) & 1) ^ 1, a.status)) return false;
           if (u == 0) {
-            // the scales: slot n_tile % 4 was read long ago (chunk slots of the
-            // tile before last are only free after its softmax)
-            const uint32_t ms = n_tile % kMetaRing;
-            ring.key_scale[ms][32 * g + lane] = scale;
+            const uint32_t ms = n_tile % kMeta;
+            ring.key_exp[ms][32 * g + lane] = e;
             __syncwarp();
             if (lane == 0) mbar_arrive(&ring.meta_full[ms]);
             ++n_tile;
           }
-          const uint32_t dst = smem_u32(ring.chunk[slot]);
+          const uint32_t dst = smem_u32(slots.chunk[slot]);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int rr = 4 * i + (lane >> 3);
             const int r = 32 * g + rr;
             cp_async16_or_zero(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
-                               reinterpret_cast<const void*>(at[i] + 128 * c), (ok_mask >> rr) & 1u);
+                               reinterpret_cast<const void*>(at[i] + 128 * u), (ok_mask >> rr) & 1u);
           }
           cp_async_arrive(&ring.full[slot]);
           ++n_chunk;

@@ -37,16 +37,16 @@
 // and large batches all fill the device. A query cut by a range end leaves
 // fp32 partial results that a second kernel joins.
 //
-// Roles: warps 0-7 softmax and epilogue (warp w: keys 32 (w & 3) .. of the tile,
-// one half of the heads each four), warp 8 MMA issue, warps 9-12 copies.
+// Roles: 16 warps (64 heads; else 8) for softmax and epilogue: warp w takes keys
+// 32 (w & 3) .. of the tile, each four warps 16 heads (8 of 16); then one warp that
+// issues the logits' MMAs, one that issues the values', and four that copy. (One
+// issuing warp that polled for whichever could go on was bound by its own
+// polling: 400 cycles a unit of 4 or 8 MMAs.)
 #include "kv8_gather.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kSoftWarps = 8;
-constexpr int kMmaWarp = 8;
-constexpr int kThreads = 32 * (kSoftWarps + 1 + kGatherWarps);
 constexpr int kMaxWorkers = 148;
 // P' is kept within [0, 2^(kRescale + kShift)]: the maximum M is only moved when a
 // tile exceeds it by 2^kRescale, and P' is scaled by 2^kShift so that e5m2's
@@ -55,26 +55,35 @@ constexpr float kRescale = 6.f;
 constexpr float kShift = 9.f;
 constexpr float kLn2 = 0.69314718055994531f;
 
+// NP: heads of a CTA, padded. The ring takes what shared memory is left by the
+// queries (2 NP x 576 bytes) and P: the tile whose logits are computed and the
+// tile whose values are still wanted make 8 slots the least that keeps the
+// tensor pipe from waiting for a copy in every tile (64 heads, 7 slots: 944 us
+// instead of the 8 slots' time for a 1021-query chunk).
 template <int NP> struct Cfg {
-  static constexpr int kRing = NP == 64 ? 7 : 9;
+  static constexpr int kHeads = NP == 16 ? 8 : 16;   // heads of a softmax warp
+  static constexpr int kSoftWarps = 4 * (NP / kHeads);
+  static constexpr int kThreads = 32 * (kSoftWarps + 2 + kGatherWarps);
+  static constexpr int kRing = NP == 64 ? 8 : NP == 32 ? 10 : 11;
+  static constexpr int kMeta = NP == 64 ? 2 : 4;
   static constexpr uint32_t kTmem = NP == 64 ? 512 : NP == 32 ? 256 : 128;
   static constexpr uint32_t kColS = 4 * NP;          // two buffers of 2 NP columns
 };
 
 template <int NP>
-struct __align__(1024) Smem {
-  Kv8Ring<Cfg<NP>::kRing> ring;
+struct Smem {
+  Kv8Slots<Cfg<NP>::kRing> slots;
   alignas(1024) uint8_t q[2 * NP * 576];
   alignas(1024) uint8_t p[kTile * 128];              // row = key: first terms at byte 0, second at 64
-  alignas(16) float head_scale[2][NP];               // logit2 = (hi + lo / 16) * 2^e * head_scale
-  alignas(16) float ref[kSoftWarps][NP / 2];         // M - kShift, a copy per warp
-  alignas(16) float alpha[kSoftWarps][NP / 2];
-  float tile_max[2][4][NP];
-  float sum[4][NP];
-  int64_t scratch[kThreads / 32 + 2];
+  Kv8Ring<Cfg<NP>::kRing, Cfg<NP>::kMeta> ring;
+  alignas(16) float head_scale[NP];                  // logit2 = (hi + lo / 16) * 2^e * head_scale
   uint64_t q_full, p_full, pv_done, drained;
   uint64_t s_full[2], s_empty[2];
   uint32_t tmem_base;
+  union {
+    float tile_max[2][4][NP];                        // also the sums at a query's end
+    int64_t scratch[Cfg<NP>::kThreads / 32 + 2];     // before the roles begin
+  };
 };
 
 // Workspace: which query each worker's first and last range end cuts, then the
@@ -127,35 +136,39 @@ struct Pieces {
 };
 
 template <int NP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<NP>::kThreads, 1)
 kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_heads, int workers) {
-  constexpr int R = Cfg<NP>::kRing;
-  constexpr int HN = NP / 2;                         // heads of a softmax warp
-  extern __shared__ uint8_t smem_raw[];
-  Smem<NP>& S = *reinterpret_cast<Smem<NP>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  using C = Cfg<NP>;
+  using Ring = Kv8Ring<C::kRing, C::kMeta>;
+  constexpr int R = C::kRing, HN = C::kHeads, kQkWarp = C::kSoftWarps, kPvWarp = kQkWarp + 1;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem<NP>& S = *reinterpret_cast<Smem<NP>*>(smem_raw);
   const int warp = warp_id(), lane = threadIdx.x & 31;
   const int worker = blockIdx.x / groups, group = blockIdx.x % groups;
   const int head0 = group * group_heads;
   const int live = min(group_heads, a.heads - head0);
   const Partials part = partials(a.ws, workers, a.heads);
+  if (smem_u32(smem_raw) & 1023u) {                  // (never: nothing static lies before it)
+    report(a.status, DSA_ERR_CUDA);
+    return;
+  }
 
-  const Kv8Range range = kv8_range<kThreads>(a.keys, a.idx != nullptr, a.k, worker, workers, S.scratch);
+  const Kv8Range range = kv8_range<C::kThreads>(a.keys, a.idx != nullptr, a.k, worker, workers, S.scratch);
   if (threadIdx.x == 0 && group == 0) part.head_item[worker] = part.tail_item[worker] = -1;
   if (range.t0 == range.t1) return;
   if (threadIdx.x == 0) {
     S.ring.init();
-    mbar_init(&S.q_full, kSoftWarps);
-    mbar_init(&S.p_full, kSoftWarps);
+    mbar_init(&S.q_full, C::kSoftWarps);
+    mbar_init(&S.p_full, C::kSoftWarps);
     mbar_init(&S.pv_done, 1);
-    mbar_init(&S.drained, 1);
+    mbar_init(&S.drained, 2);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&S.s_full[b], 1);
-      mbar_init(&S.s_empty[b], kSoftWarps);
+      mbar_init(&S.s_empty[b], C::kSoftWarps);
     }
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) tmem_alloc(&S.tmem_base, Cfg<NP>::kTmem);
+  if (warp == kQkWarp) tmem_alloc(&S.tmem_base, C::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -163,152 +176,134 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
   Pieces pieces(a, range);
   Piece pc;
 
-  if (warp > kMmaWarp) {
+  if (warp > kPvWarp) {
     // ------------------------------------------------------------ copies
-    Kv8Gather<R> g{S.ring, a, lane, warp - kMmaWarp - 1};
+    Kv8Gather<Ring> g{S.ring, S.slots, a, lane, warp - kPvWarp - 1};
     while (pieces.next(pc))
       if (!g.run(pc.qi, pc.j0, pc.n)) break;
     g.drain();
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issue
-    // Per tile: S^T(g) over chunks 0-2 and the rope columns; O^T += V^T P of the
-    // tile before over chunk 0, which frees the slot that chunk 3 of tile g may
-    // still wait for; chunk 3; the rest of the tile before. The softmax of tile g
-    // then has the value products of g - 1 and the logits of g + 1 to hide behind.
-    constexpr uint32_t idesc_qk = make_idesc(2 * NP, 0, 0, 0, 0);
-    constexpr uint32_t idesc_pv = make_idesc(NP, 0, 1, 1, 1);   // e4m3 codes, e5m2 probabilities
+  } else if (warp == kQkWarp) {
+    // ------------------------------------------------------------ S^T = K Q^T
+    constexpr uint32_t idesc = make_idesc(2 * NP, 0, 0, 0, 0);
     const uint64_t q_desc = sw128_desc(smem_u32(S.q), 16, 1024);
     const uint64_t qr_desc = sw64_desc(smem_u32(S.q) + 4 * (2 * NP * 128));
-    const uint64_t p_desc = sw128_desc(smem_u32(S.p), 16384, 1024);
-    const uint64_t k_desc = sw128_desc(smem_u32(S.ring.chunk[0]), 16384, 1024);
-    const uint64_t r_desc = sw64_desc(smem_u32(S.ring.rope[0]));
-    uint32_t g = 0;                                  // tiles begun
-    uint32_t ck = 0, cv = 0;                         // chunks taken by the logits, by the values
-    uint32_t n_piece = 0;
+    const uint64_t k_desc = sw128_desc(smem_u32(S.slots.chunk[0]), 16384, 1024);
+    const uint64_t r_desc = sw64_desc(smem_u32(S.slots.rope));
+    uint32_t g = 0, slot = 0, phase = 0, n_piece = 0;
     bool ok = true;
-
-    auto qk_chunk = [&](int c) -> bool {
-      const uint32_t slot = ck % R;
-      if (!mbar_wait_warp(&S.ring.full[slot], (ck / R) & 1, a.status)) return false;
-      fence_proxy_async_smem();                      // the copies, before the MMAs read them
-      tc_fence_after();
-      const uint64_t kd = k_desc + slot * (kChunkB / 16), qd = q_desc + c * (2 * NP * 128 / 16);
-      const uint32_t d = tmem + Cfg<NP>::kColS + (g & 1) * (2 * NP);
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mma_f8(d, kd + 2 * k, qd + 2 * k, idesc_qk, c > 0 || k > 0);
-      }
-      __syncwarp();
-      ++ck;
-      return true;
-    };
-    auto pv_chunk = [&](int c, bool first) {
-      const uint32_t slot = cv % R;
-      const uint64_t vd = k_desc + slot * (kChunkB / 16);
-      const uint32_t d = tmem + c * NP;
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          mma_f8(d, vd + 256 * k, p_desc + 256 * k, idesc_pv, !first || k > 0);
-          mma_f8(d, vd + 256 * k, p_desc + 256 * k + 4, idesc_pv, 1);
-        }
-        mma_commit(&S.ring.empty[slot]);
-        if (c == 3) mma_commit(&S.pv_done);
-      }
-      __syncwarp();
-      ++cv;
-    };
-    auto p_ready = [&](uint32_t tile) -> bool {
-      if (!mbar_wait_warp(&S.p_full, tile & 1, a.status)) return false;
-      tc_fence_after();
-      return true;
-    };
-
     while (ok && pieces.next(pc)) {
       ok = mbar_wait_warp(&S.q_full, n_piece & 1, a.status);
       ++n_piece;
-      for (int j = 0; j < pc.n && ok; ++j) {
+      for (int j = 0; j < pc.n && ok; ++j, ++g) {
+        const uint32_t d = tmem + C::kColS + (g & 1) * (2 * NP);
         ok = mbar_wait_warp(&S.s_empty[g & 1], ((g >> 1) & 1) ^ 1, a.status);
-        for (int c = 0; c < 3 && ok; ++c) ok = qk_chunk(c);
-        if (!ok) break;
-        const uint32_t rs = g % kRopeRing;
-        ok = mbar_wait_warp(&S.ring.rope_full[rs], (g / kRopeRing) & 1, a.status);
-        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          ok = ok && mbar_wait_warp(&S.ring.full[slot], phase, a.status);
+          fence_proxy_async_smem();                  // the copies, before the MMAs read them
+          tc_fence_after();
+          const uint64_t kd = k_desc + slot * (kChunkB / 16), qd = q_desc + c * (2 * NP * 128 / 16);
+          if (ok && elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f8(d, kd + 2 * k, qd + 2 * k, idesc, (c | k) != 0);
+          }
+          __syncwarp();
+          if (++slot == R) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+        ok = ok && mbar_wait_warp(&S.ring.rope_full, g & 1, a.status);
         fence_proxy_async_smem();
         tc_fence_after();
-        if (elect_one()) {
-          const uint32_t d = tmem + Cfg<NP>::kColS + (g & 1) * (2 * NP);
-          const uint64_t rd = r_desc + rs * (kRopeB / 16);
+        if (ok && elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) mma_f8(d, rd + 2 * k, qr_desc + 2 * k, idesc_qk, 1);
-          mma_commit(&S.ring.rope_empty[rs]);
+          for (int k = 0; k < 2; ++k) mma_f8(d, r_desc + 2 * k, qr_desc + 2 * k, idesc, 1);
+          mma_commit(&S.s_full[g & 1]);
+          mma_commit(&S.ring.rope_empty);
         }
         __syncwarp();
-        if (j > 0) {
-          ok = p_ready(g - 1);
-          if (!ok) break;
-          pv_chunk(0, j == 1);
-        }
-        ok = qk_chunk(3);
-        if (!ok) break;
-        if (elect_one()) mma_commit(&S.s_full[g & 1]);
-        __syncwarp();
-        if (j > 0)
-          for (int c = 1; c < 4; ++c) pv_chunk(c, j == 1);
-        ++g;
       }
-      if (ok) ok = p_ready(g - 1);
-      if (ok)
-        for (int c = 0; c < 4; ++c) pv_chunk(c, pc.n == 1);
     }
     // nothing is in flight when the block ends, whichever way it got here
     if (elect_one()) mma_commit(&S.drained);
     __syncwarp();
     mbar_wait_warp(&S.drained, 0, a.status);
+  } else if (warp == kPvWarp) {
+    // ------------------------------------------------------------ O^T += V^T P
+    constexpr uint32_t idesc = make_idesc(NP, 0, 1, 1, 1);   // e4m3 codes, e5m2 probabilities
+    const uint64_t p_desc = sw128_desc(smem_u32(S.p), 16384, 1024);
+    const uint64_t v_desc = sw128_desc(smem_u32(S.slots.chunk[0]), 16384, 1024);
+    uint32_t g = 0, slot = 0;
+    bool ok = true;
+    while (ok && pieces.next(pc)) {
+      for (int j = 0; j < pc.n && ok; ++j, ++g) {
+        ok = mbar_wait_warp(&S.p_full, g & 1, a.status);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint64_t vd = v_desc + slot * (kChunkB / 16);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              mma_f8(tmem + c * NP, vd + 256 * k, p_desc + 256 * k, idesc, k > 0 || j > 0);
+              mma_f8(tmem + c * NP, vd + 256 * k, p_desc + 256 * k + 4, idesc, 1);
+            }
+            mma_commit(&S.ring.empty[slot]);
+            if (c == 3) mma_commit(&S.pv_done);
+          }
+          __syncwarp();
+          if (++slot == R) slot = 0;
+        }
+      }
+    }
+    if (elect_one()) mma_commit(&S.drained);
+    __syncwarp();
+    mbar_wait_warp(&S.drained, 0, a.status);
   } else {
     // ------------------------------------------------------------ softmax and epilogue
-    const int sub = warp & 3, half = warp >> 2;
+    const int sub = warp & 3;
     const int key = 32 * sub + lane;                 // this thread's key of each tile
-    const int hb = half * HN;                        // first head of this warp's half
+    const int hb = (warp >> 2) * HN;                 // first of this warp's heads
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * sub) << 16);
-    const uint32_t s_col = Cfg<NP>::kColS + hb;
+    const uint32_t s_col = C::kColS + hb;
     uint8_t* const p_row = S.p + key * 128;
     const uint32_t sw = key & 7;
-    const uint32_t bar = 1 + half;                   // the four warps of a half
-    uint32_t g = 0, n_piece = 0;
+    const uint32_t bar = 1 + (warp >> 2);            // the four warps of these heads
+    constexpr uint32_t kBarAll = 1 + NP / HN;        // all softmax warps
+    uint32_t g = 0;
     bool ok = true;
     bool more = pieces.next(pc);
 
-    auto stage_q = [&](const Piece& p, uint32_t n) {
+    auto stage_q = [&](const Piece& p) {
       const __nv_bfloat16* q = a.q + static_cast<int64_t>(p.qi) * a.ld_q +
                                static_cast<int64_t>(head0) * kRow8;
-      stage_q8<NP>(S.q, q, live, warp, kSoftWarps, lane, [&](int h, int s) {
-        S.head_scale[n & 1][h] = a.scale_log2 * pow2i(s);
-      });
+      stage_q8<NP>(S.q, q, live, warp, C::kSoftWarps, lane,
+                   [&](int h, int s) { S.head_scale[h] = a.scale_log2 * pow2i(s); });
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.q_full);
-      named_bar_sync(3, 32 * kSoftWarps);            // head_scale is complete
+      named_bar_sync(kBarAll, 32 * C::kSoftWarps);   // head_scale is complete
     };
-    stage_q(pc, 0);
+    stage_q(pc);
 
-    while (more && ok) {
-      const float* const hs = S.head_scale[n_piece & 1] + hb;
-      float m_used = -INFINITY;                      // lane h < HN: running maximum of head hb + h
+    // After a wait that ran out (reported) these warps go on without waiting: the
+    // named barriers that they share are not bounded, so all of them must take
+    // the same steps to the end.
+    while (more) {
+      float m_used = -INFINITY;                      // lane h % HN: running maximum of head hb + h
       float l[HN];
 #pragma unroll
       for (int i = 0; i < HN; ++i) l[i] = 0.f;
       for (int j = 0; j < pc.n; ++j, ++g) {
         const uint32_t b = g & 1;
-        if (!mbar_wait_warp(&S.ring.meta_full[g % kMetaRing], (g / kMetaRing) & 1, a.status) ||
-            !mbar_wait_warp(&S.s_full[b], (g >> 1) & 1, a.status)) {
-          ok = false;
-          break;
-        }
+        ok = ok && mbar_wait_warp(&S.ring.meta_full[g % C::kMeta], (g / C::kMeta) & 1, a.status) &&
+             mbar_wait_warp(&S.s_full[b], (g >> 1) & 1, a.status);
         tc_fence_after();
-        const float ks = S.ring.key_scale[g % kMetaRing][key];
-        const bool valid = ks > 0.f;
-        const float e_key = static_cast<float>(static_cast<int>(__float_as_uint(ks) >> 23) - 127);
+        const int e_key = S.ring.key_exp[g % C::kMeta][key];
+        const bool valid = e_key != kNoKey;
+        const float ks = valid ? pow2i(e_key) : 0.f, e_add = valid ? static_cast<float>(e_key) : -INFINITY;
         float y[HN];
         {
           uint32_t v[HN], w[HN];
@@ -318,15 +313,15 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.s_empty[b]);
-          const float4* h4 = reinterpret_cast<const float4*>(hs);
+          const float4* h4 = reinterpret_cast<const float4*>(S.head_scale + hb);
 #pragma unroll
           for (int i = 0; i < HN; i += 4) {
             const float4 f = h4[i / 4];
             const float ff[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-              const float s = fmaf(__uint_as_float(w[i + t]), 0.0625f, __uint_as_float(v[i + t])) * ks;
-              y[i + t] = valid ? fmaf(s, ff[t], e_key) : -INFINITY;
+              const float s = fmaf(__uint_as_float(w[i + t]), 0.0625f, __uint_as_float(v[i + t]));
+              y[i + t] = fmaf(s * ks, ff[t], e_add);
             }
           }
         }
@@ -335,61 +330,43 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
 #pragma unroll
         for (int i = 0; i < HN; ++i) {
           const float m = warp_max(y[i]);
-          if (lane == i) mine = m;
+          if (lane % HN == i) mine = m;
         }
         if (lane < HN) S.tile_max[b][sub][hb + lane] = mine;
         named_bar_sync(bar, 128);
         float mx = -INFINITY;
-        if (lane < HN)
 #pragma unroll
-          for (int w = 0; w < 4; ++w) mx = fmaxf(mx, S.tile_max[b][w][hb + lane]);
+        for (int w = 0; w < 4; ++w) mx = fmaxf(mx, S.tile_max[b][w][hb + lane % HN]);
         const bool move = mx > m_used + kRescale;    // (true for the first key: m_used = -inf)
         const float m_next = move ? mx : m_used;
         const float alpha = move ? ex2(m_used - m_next) : 1.f;
         m_used = m_next;
-        if (lane < HN) {
-          S.ref[warp][lane] = m_next == -INFINITY ? 0.f : m_next - kShift;
-          S.alpha[warp][lane] = alpha;
-        }
-        __syncwarp();
-        const bool rescale = __any_sync(0xffffffffu, move && lane < HN) && j > 0;
+        const float ref = m_next == -INFINITY ? 0.f : m_next - kShift;
+        const bool rescale = __any_sync(0xffffffffu, move) && j > 0;
         if (rescale) {
-          const float4* a4 = reinterpret_cast<const float4*>(S.alpha[warp]);
 #pragma unroll
-          for (int i = 0; i < HN; i += 4) {
-            const float4 f = a4[i / 4];
-            l[i] *= f.x;
-            l[i + 1] *= f.y;
-            l[i + 2] *= f.z;
-            l[i + 3] *= f.w;
-          }
+          for (int i = 0; i < HN; ++i) l[i] *= __shfl_sync(0xffffffffu, alpha, i);
         }
         // P' and its two terms
         uint32_t hi[HN / 4], lo[HN / 4];
-        const float inv_scale = valid ? pow2i(-static_cast<int>(e_key)) : 0.f;
-        const float4* r4 = reinterpret_cast<const float4*>(S.ref[warp]);
+        const float inv_scale = valid ? pow2i(-e_key) : 0.f;
 #pragma unroll
         for (int i = 0; i < HN; i += 4) {
-          const float4 r = r4[i / 4];
-          const float p0 = ex2(y[i] - r.x), p1 = ex2(y[i + 1] - r.y);
-          const float p2 = ex2(y[i + 2] - r.z), p3 = ex2(y[i + 3] - r.w);
-          l[i] = fmaf(p0, inv_scale, l[i]);
-          l[i + 1] = fmaf(p1, inv_scale, l[i + 1]);
-          l[i + 2] = fmaf(p2, inv_scale, l[i + 2]);
-          l[i + 3] = fmaf(p3, inv_scale, l[i + 3]);
-          const uint32_t h0 = to_e5m2x2(p0, p1), h1 = to_e5m2x2(p2, p3);
+          float p[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            p[t] = ex2(y[i + t] - __shfl_sync(0xffffffffu, ref, i + t));
+            l[i + t] = fmaf(p[t], inv_scale, l[i + t]);
+          }
+          const uint32_t h0 = to_e5m2x2(p[0], p[1]), h1 = to_e5m2x2(p[2], p[3]);
           const float2 b0 = from_e5m2x2(h0), b1 = from_e5m2x2(h1);
           hi[i / 4] = h0 | (h1 << 16);
-          lo[i / 4] = to_e5m2x2(p0 - b0.x, p1 - b0.y) | (to_e5m2x2(p2 - b1.x, p3 - b1.y) << 16);
+          lo[i / 4] = to_e5m2x2(p[0] - b0.x, p[1] - b0.y) | (to_e5m2x2(p[2] - b1.x, p[3] - b1.y) << 16);
         }
         // the value products of the tile before are done: P and O may be written
-        if (g > 0 && !mbar_wait_warp(&S.pv_done, (g - 1) & 1, a.status)) {
-          ok = false;
-          break;
-        }
+        if (g > 0) ok = ok && mbar_wait_warp(&S.pv_done, (g - 1) & 1, a.status);
         if (rescale) {
           tc_fence_after();
-          const float4* a4 = reinterpret_cast<const float4*>(S.alpha[warp]);
 #pragma unroll 1
           for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -397,89 +374,75 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
               uint32_t o[8];
               tmem_ld8(t_lane + c * NP + hb + i, o);
               tmem_wait_ld();
-              const float4 f0 = a4[i / 4], f1 = a4[i / 4 + 1];
-              const float ff[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-              for (int t = 0; t < 8; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * ff[t]);
+              for (int t = 0; t < 8; ++t)
+                o[t] = __float_as_uint(__uint_as_float(o[t]) * __shfl_sync(0xffffffffu, alpha, i + t));
               tmem_st8(t_lane + c * NP + hb + i, o);
             }
           tmem_wait_st();
         }
         if constexpr (HN == 8) {
-          const uint32_t at = ((0 ^ sw) << 4) + hb, at2 = ((4 ^ sw) << 4) + hb;
-          *reinterpret_cast<uint2*>(p_row + at) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(p_row + at2) = make_uint2(lo[0], lo[1]);
+          *reinterpret_cast<uint2*>(p_row + (sw << 4) + hb) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(p_row + ((4 ^ sw) << 4) + hb) = make_uint2(lo[0], lo[1]);
         } else {
-#pragma unroll
-          for (int i = 0; i < HN / 16; ++i) {
-            const uint32_t c = hb / 16 + i;
-            *reinterpret_cast<uint4*>(p_row + ((c ^ sw) << 4)) =
-                make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-            *reinterpret_cast<uint4*>(p_row + (((c + 4) ^ sw) << 4)) =
-                make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-          }
+          const uint32_t c = hb / 16;
+          *reinterpret_cast<uint4*>(p_row + ((c ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(p_row + (((c + 4) ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.p_full);
       }
-      if (!ok) break;
       // the next query's logits may start while this one's result is written out
       const Piece done = pc;
       more = pieces.next(pc);
-      if (more) stage_q(pc, n_piece + 1);
-      ++n_piece;
+      named_bar_sync(kBarAll, 32 * C::kSoftWarps);   // head_scale and S.q have been used
+      if (more) stage_q(pc);
 
       // sums over the keys: lanes, then the four warps in order
       const float lw = reduce_columns<HN>(l, lane);
-      if (lane < HN) S.sum[sub][hb + lane] = lw;
+      if (lane < HN) S.tile_max[g & 1][sub][hb + lane] = lw;
       named_bar_sync(bar, 128);
       const bool cut = done.n < done.tiles;
-      const int slot = 2 * worker + (done.j0 == 0 ? 1 : 0);
-      if (lane < HN) {
-        const float lt = ((S.sum[0][hb + lane] + S.sum[1][hb + lane]) + S.sum[2][hb + lane]) +
-                         S.sum[3][hb + lane];
-        const float ref = m_used == -INFINITY ? 0.f : m_used - kShift;
-        S.alpha[warp][lane] = lt == 0.f ? 0.f : 1.f / lt;
-        if (sub == 0 && hb + lane < live) {
-          const int64_t h = head0 + hb + lane;
-          if (cut)
-            part.ml[static_cast<int64_t>(slot) * a.heads + h] = make_float2(ref, lt);
-          else if (a.lse != nullptr)
-            a.lse[static_cast<int64_t>(done.qi) * a.heads + h] =
-                lt == 0.f ? -INFINITY : (ref + log2f(lt)) * kLn2;
-        }
+      const int64_t slot = 2 * worker + (done.j0 == 0 ? 1 : 0);
+      const float* const sums = &S.tile_max[g & 1][0][hb + lane % HN];
+      const float lt = ((sums[0] + sums[NP]) + sums[2 * NP]) + sums[3 * NP];
+      const float ref = m_used == -INFINITY ? 0.f : m_used - kShift;
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      if (sub == 0 && lane < HN && hb + lane < live) {
+        const int64_t h = head0 + hb + lane;
+        if (cut)
+          part.ml[slot * a.heads + h] = make_float2(ref, lt);
+        else if (a.lse != nullptr)
+          a.lse[static_cast<int64_t>(done.qi) * a.heads + h] =
+              lt == 0.f ? -INFINITY : (ref + log2f(lt)) * kLn2;
       }
-      __syncwarp();
-      if (!mbar_wait_warp(&S.pv_done, (g - 1) & 1, a.status)) {
-        ok = false;
-        break;
-      }
+      ok = ok && mbar_wait_warp(&S.pv_done, (g - 1) & 1, a.status);
       tc_fence_after();
       // O^T: lane = value column, TMEM column = head
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         const int dim = c * 128 + 32 * sub + lane;
-#pragma unroll 1
-        for (int i = 0; i < HN; i += 8) {
-          uint32_t o[8];
-          tmem_ld8(t_lane + c * NP + hb + i, o);
-          tmem_wait_ld();
+        uint32_t o[HN];
+        tmem_ld<HN>(t_lane + c * NP + hb, o);
+        tmem_wait_ld();
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            if (hb + i + t >= live) break;
-            const int64_t h = head0 + hb + i + t;
-            const float v = __uint_as_float(o[t]);
+        for (int t = 0; t < HN; ++t) {
+          const float f = __shfl_sync(0xffffffffu, inv, t);
+          const float v = __uint_as_float(o[t]);
+          if (hb + t < live) {
+            const int64_t h = head0 + hb + t;
             if (cut)
-              part.o[(static_cast<int64_t>(slot) * a.heads + h) * 512 + dim] = v;
+              part.o[(slot * a.heads + h) * 512 + dim] = v;
             else
               a.out[(static_cast<int64_t>(done.qi) * a.heads + h) * 512 + dim] =
-                  __float2bfloat16(S.alpha[warp][i + t] == 0.f ? 0.f : v * S.alpha[warp][i + t]);
+                  __float2bfloat16(f == 0.f ? 0.f : v * f);
           }
         }
       }
       tc_fence_before();
+      named_bar_sync(bar, 128);                      // the sums have been read
       if (threadIdx.x == 0 && group == 0) {
         if (cut && done.j0 > 0) {
           part.head_item[worker] = done.qi;
@@ -492,9 +455,9 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, Cfg<NP>::kTmem);
+    tmem_dealloc(tmem, C::kTmem);
   }
 }
 
@@ -559,12 +522,12 @@ Split split(int32_t n_q, int32_t heads, int64_t max_keys, int num_sms) {
 
 template <int NP>
 cudaError_t launch(const Kv8AttnArgs& a, const Split& s, cudaStream_t stream) {
-  const size_t smem = sizeof(Smem<NP>) + 1024;
-  static_assert(sizeof(Smem<NP>) + 1024 <= 232448, "shared memory of one SM");
+  const size_t smem = sizeof(Smem<NP>);
+  static_assert(sizeof(Smem<NP>) <= 232448, "shared memory of one CTA");
   cudaError_t e = cudaFuncSetAttribute(kv8_mqa_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  kv8_mqa_kernel<NP><<<s.workers * s.groups, kThreads, smem, stream>>>(a, s.groups, s.group_heads, s.workers);
+  kv8_mqa_kernel<NP><<<s.workers * s.groups, Cfg<NP>::kThreads, smem, stream>>>(a, s.groups, s.group_heads, s.workers);
   return cudaGetLastError();
 }
 
