@@ -122,6 +122,18 @@ __device__ __forceinline__ float warp_max(float x) {
   return r;
 }
 
+// Whether any thread of the named barrier's has v; waits for all of them.
+__device__ __forceinline__ bool named_bar_any(uint32_t id, uint32_t threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -253,45 +265,64 @@ __device__ __forceinline__ Kv8Range kv8_range(const KeySide& ks, bool sparse, in
 // are as exact as the codes themselves. Four 128-byte-swizzled chunks of 128
 // columns, 2 ROWS rows each, then the rope columns in 64-byte rows.
 // Returns through set(h, s) the exponent of each head. An infinity or NaN makes
-// the whole head NaN. Warps `warp`, warp + warps, ... take one head at a time.
-template <int ROWS, typename F>
+// the whole head NaN. Warp `warp` of WARPS takes heads warp, warp + WARPS, ...
+// Up to four heads are fetched at a time, before any of them is converted.
+template <int ROWS, int WARPS, typename F>
 __device__ __forceinline__ void stage_q8(uint8_t* tile, const __nv_bfloat16* q, int live, int warp,
-                                         int warps, int lane, F set) {
+                                         int lane, F set) {
   constexpr int kChunk = 2 * ROWS * 128;
-  for (int h = warp; h < ROWS; h += warps) {
-    uint32_t w[9];
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(h) * kRow8);
+  constexpr int kPerWarp = ROWS / WARPS, kBatch = kPerWarp < 4 ? kPerWarp : 4;
+  static_assert(ROWS % WARPS == 0 && kPerWarp % kBatch == 0, "");
+#pragma unroll 1
+  for (int r0 = 0; r0 < kPerWarp; r0 += kBatch) {
+    uint32_t w[kBatch][9];
 #pragma unroll
-    for (int i = 0; i < 9; ++i) w[i] = h < live ? __ldg(src + lane + 32 * i) : 0u;
-    uint32_t m = 0;
+    for (int r = 0; r < kBatch; ++r) {
+      const int h = warp + WARPS * (r0 + r);
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(h) * kRow8);
 #pragma unroll
-    for (int i = 0; i < 9; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-    m = __reduce_max_sync(0xffffffffu, m);
-    const bool bad = m >= 0x7f80u;
-    const int s = min(max(static_cast<int>(m >> 7) - 127 - 7, -120), 120);
-    const float f = pow2i(-s);
-#pragma unroll
-    for (int i = 0; i < 9; ++i) {
-      const float x = __uint_as_float(w[i] << 16) * f, y = __uint_as_float(w[i] & 0xffff0000u) * f;
-      uint32_t hi = to_e4m3x2(x, y);
-      const float2 b = from_e4m3x2(hi);
-      uint32_t lo = to_e4m3x2((x - b.x) * 16.f, (y - b.y) * 16.f);
-      if (bad) hi = lo = 0x7f7fu;
-      const int col = 2 * (lane + 32 * i);
-      uint8_t* at;
-      int step;                                     // from the first term's row to the second's
-      if (i < 8) {
-        at = tile + (col >> 7) * kChunk + h * 128 + ((((col & 127) >> 4) ^ (h & 7)) << 4);
-        step = ROWS * 128;
-      } else {
-        at = tile + 4 * kChunk + h * 64 + ((((col - 512) >> 4) ^ ((h >> 1) & 3)) << 4);
-        step = ROWS * 64;
-      }
-      *reinterpret_cast<uint16_t*>(at + (col & 15)) = static_cast<uint16_t>(hi);
-      *reinterpret_cast<uint16_t*>(at + step + (col & 15)) = static_cast<uint16_t>(lo);
+      for (int i = 0; i < 9; ++i) w[r][i] = h < live ? __ldg(src + lane + 32 * i) : 0u;
     }
-    if (lane == 0) set(h, s);
+#pragma unroll
+    for (int r = 0; r < kBatch; ++r) {
+      const int h = warp + WARPS * (r0 + r);
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 9; ++i) m = max(m, max(w[r][i] & 0x7fffu, (w[r][i] >> 16) & 0x7fffu));
+      m = __reduce_max_sync(0xffffffffu, m);
+      const bool bad = m >= 0x7f80u;
+      const int s = min(max(static_cast<int>(m >> 7) - 127 - 7, -120), 120);
+      const float f = pow2i(-s);
+#pragma unroll
+      for (int i = 0; i < 9; ++i) {
+        const float x = __uint_as_float(w[r][i] << 16) * f, y = __uint_as_float(w[r][i] & 0xffff0000u) * f;
+        uint32_t hi = to_e4m3x2(x, y);
+        const float2 b = from_e4m3x2(hi);
+        uint32_t lo = to_e4m3x2((x - b.x) * 16.f, (y - b.y) * 16.f);
+        if (bad) hi = lo = 0x7f7fu;
+        const int col = 2 * (lane + 32 * i);
+        uint8_t* at;
+        int step;                                   // from the first term's row to the second's
+        if (i < 8) {
+          at = tile + (col >> 7) * kChunk + h * 128 + ((((col & 127) >> 4) ^ (h & 7)) << 4);
+          step = ROWS * 128;
+        } else {
+          at = tile + 4 * kChunk + h * 64 + ((((col - 512) >> 4) ^ ((h >> 1) & 3)) << 4);
+          step = ROWS * 64;
+        }
+        *reinterpret_cast<uint16_t*>(at + (col & 15)) = static_cast<uint16_t>(hi);
+        *reinterpret_cast<uint16_t*>(at + step + (col & 15)) = static_cast<uint16_t>(lo);
+      }
+      if (lane == 0) set(h, s);
+    }
   }
+}
+
+// Fetches `live` heads of a query into L2 (for stage_q8), `lanes` threads sharing the lines.
+__device__ __forceinline__ void prefetch_q8(const __nv_bfloat16* q, int live, int lane, int lanes) {
+  const char* p = reinterpret_cast<const char*>(q);
+  for (int i = 128 * lane; i < live * kRow8 * 2; i += 128 * lanes)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
 }
 
 }  // namespace dsa

@@ -42,6 +42,8 @@
 // issues the logits' MMAs, one that issues the values', and four that copy. (One
 // issuing warp that polled for whichever could go on was bound by its own
 // polling: 400 cycles a unit of 4 or 8 MMAs.)
+#include <cfloat>
+
 #include "kv8_gather.cuh"
 
 namespace dsa {
@@ -179,8 +181,12 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
   if (warp > kPvWarp) {
     // ------------------------------------------------------------ copies
     Kv8Gather<Ring> g{S.ring, S.slots, a, lane, warp - kPvWarp - 1};
-    while (pieces.next(pc))
+    while (pieces.next(pc)) {
+      if (pieces.left > 0)                           // the next query, for its staging
+        prefetch_q8(a.q + static_cast<int64_t>(pc.qi + 1) * a.ld_q + static_cast<int64_t>(head0) * kRow8,
+                    live, 32 * g.g + lane, 32 * kGatherWarps);
       if (!g.run(pc.qi, pc.j0, pc.n)) break;
+    }
     g.drain();
   } else if (warp == kQkWarp) {
     // ------------------------------------------------------------ S^T = K Q^T
@@ -279,7 +285,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
     auto stage_q = [&](const Piece& p) {
       const __nv_bfloat16* q = a.q + static_cast<int64_t>(p.qi) * a.ld_q +
                                static_cast<int64_t>(head0) * kRow8;
-      stage_q8<NP>(S.q, q, live, warp, C::kSoftWarps, lane,
+      stage_q8<NP, C::kSoftWarps>(S.q, q, live, warp, lane,
                    [&](int h, int s) { S.head_scale[h] = a.scale_log2 * pow2i(s); });
       fence_proxy_async_smem();
       __syncwarp();
@@ -325,43 +331,58 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
             }
           }
         }
-        // maximum of each head over the tile's 128 keys
-        float mine = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < HN; ++i) {
-          const float m = warp_max(y[i]);
-          if (lane % HN == i) mine = m;
-        }
-        if (lane < HN) S.tile_max[b][sub][hb + lane] = mine;
-        named_bar_sync(bar, 128);
-        float mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) mx = fmaxf(mx, S.tile_max[b][w][hb + lane % HN]);
-        const bool move = mx > m_used + kRescale;    // (true for the first key: m_used = -inf)
-        const float m_next = move ? mx : m_used;
-        const float alpha = move ? ex2(m_used - m_next) : 1.f;
-        m_used = m_next;
-        const float ref = m_next == -INFINITY ? 0.f : m_next - kShift;
-        const bool rescale = __any_sync(0xffffffffu, move) && j > 0;
-        if (rescale) {
-#pragma unroll
-          for (int i = 0; i < HN; ++i) l[i] *= __shfl_sync(0xffffffffu, alpha, i);
-        }
-        // P' and its two terms
+        // P' and its two terms, with the maximum as it stands; where that is more
+        // than 2^kRescale too low (in a query's first tile, and at a head's first
+        // key, always) it is found anew
         uint32_t hi[HN / 4], lo[HN / 4];
         const float inv_scale = valid ? pow2i(-e_key) : 0.f;
+        float alpha = 1.f;
+        bool rescale = false;
+        auto weigh = [&](float ref, bool add) {
+          bool over = false;
+          float pl[HN];
 #pragma unroll
-        for (int i = 0; i < HN; i += 4) {
-          float p[4];
+          for (int i = 0; i < HN; i += 4) {
+            float p[4];
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            p[t] = ex2(y[i + t] - __shfl_sync(0xffffffffu, ref, i + t));
-            l[i + t] = fmaf(p[t], inv_scale, l[i + t]);
+            for (int t = 0; t < 4; ++t) {
+              const float x = y[i + t] - __shfl_sync(0xffffffffu, ref, i + t);
+              over |= x > kRescale + kShift;
+              p[t] = ex2(x);
+              pl[i + t] = p[t];
+            }
+            const uint32_t h0 = to_e5m2x2(p[0], p[1]), h1 = to_e5m2x2(p[2], p[3]);
+            const float2 b0 = from_e5m2x2(h0), b1 = from_e5m2x2(h1);
+            hi[i / 4] = h0 | (h1 << 16);
+            lo[i / 4] = to_e5m2x2(p[0] - b0.x, p[1] - b0.y) | (to_e5m2x2(p[2] - b1.x, p[3] - b1.y) << 16);
           }
-          const uint32_t h0 = to_e5m2x2(p[0], p[1]), h1 = to_e5m2x2(p[2], p[3]);
-          const float2 b0 = from_e5m2x2(h0), b1 = from_e5m2x2(h1);
-          hi[i / 4] = h0 | (h1 << 16);
-          lo[i / 4] = to_e5m2x2(p[0] - b0.x, p[1] - b0.y) | (to_e5m2x2(p[2] - b1.x, p[3] - b1.y) << 16);
+          const bool again = !add && named_bar_any(bar, 128, over);
+          if (!again)
+#pragma unroll
+            for (int i = 0; i < HN; ++i) l[i] = fmaf(pl[i], inv_scale, l[i]);
+          return again;
+        };
+        if (j == 0 || weigh(m_used == -INFINITY ? -FLT_MAX : m_used - kShift, false)) {
+          float mine = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < HN; ++i) {
+            const float m = warp_max(y[i]);
+            if (lane % HN == i) mine = m;
+          }
+          if (lane < HN) S.tile_max[b][sub][hb + lane] = mine;
+          named_bar_sync(bar, 128);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) mx = fmaxf(mx, S.tile_max[b][w][hb + lane % HN]);
+          const float m_next = mx > m_used ? mx : m_used;
+          alpha = mx > m_used ? ex2(m_used - m_next) : 1.f;
+          m_used = m_next;
+          rescale = j > 0;
+          if (rescale) {
+#pragma unroll
+            for (int i = 0; i < HN; ++i) l[i] *= __shfl_sync(0xffffffffu, alpha, i);
+          }
+          weigh(m_next == -INFINITY ? 0.f : m_next - kShift, true);
         }
         // the value products of the tile before are done: P and O may be written
         if (g > 0) ok = ok && mbar_wait_warp(&S.pv_done, (g - 1) & 1, a.status);
@@ -421,25 +442,45 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
       ok = ok && mbar_wait_warp(&S.pv_done, (g - 1) & 1, a.status);
       tc_fence_after();
       // O^T: lane = value column, TMEM column = head
+      if (cut) {
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        const int dim = c * 128 + 32 * sub + lane;
-        uint32_t o[HN];
-        tmem_ld<HN>(t_lane + c * NP + hb, o);
-        tmem_wait_ld();
+        for (int c = 0; c < 4; ++c) {
+          const int dim = c * 128 + 32 * sub + lane;
+          uint32_t o[HN];
+          tmem_ld<HN>(t_lane + c * NP + hb, o);
+          tmem_wait_ld();
+          float* dst = part.o + (slot * a.heads + head0 + hb) * 512 + dim;
 #pragma unroll
-        for (int t = 0; t < HN; ++t) {
-          const float f = __shfl_sync(0xffffffffu, inv, t);
-          const float v = __uint_as_float(o[t]);
-          if (hb + t < live) {
-            const int64_t h = head0 + hb + t;
-            if (cut)
-              part.o[(slot * a.heads + h) * 512 + dim] = v;
-            else
-              a.out[(static_cast<int64_t>(done.qi) * a.heads + h) * 512 + dim] =
-                  __float2bfloat16(f == 0.f ? 0.f : v * f);
-          }
+          for (int t = 0; t < HN; ++t)
+            if (hb + t < live) dst[t * 512] = __uint_as_float(o[t]);
         }
+      } else {
+        // rows of 128 columns go through the P tile (its last reader is done), so
+        // that a warp stores whole lines instead of 64 bytes of each head
+        __nv_bfloat16* const buf = reinterpret_cast<__nv_bfloat16*>(S.p) + hb * 128;
+        const int t4 = threadIdx.x & 127;
+        __nv_bfloat16* const out = a.out + (static_cast<int64_t>(done.qi) * a.heads + head0 + hb) * 512;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[HN];
+          tmem_ld<HN>(t_lane + c * NP + hb, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int t = 0; t < HN; ++t) {
+            const float f = __shfl_sync(0xffffffffu, inv, t);
+            buf[t * 128 + 32 * sub + lane] = __float2bfloat16(f == 0.f ? 0.f : __uint_as_float(o[t]) * f);
+          }
+          named_bar_sync(bar, 128);
+#pragma unroll
+          for (int i = 0; i < HN / 8; ++i) {
+            const int t = 8 * i + (t4 >> 4);
+            if (hb + t < live)
+              *reinterpret_cast<uint4*>(out + t * 512 + c * 128 + 8 * (t4 & 15)) =
+                  *reinterpret_cast<const uint4*>(buf + t * 128 + 8 * (t4 & 15));
+          }
+          named_bar_sync(bar, 128);
+        }
+        named_bar_sync(kBarAll, 32 * C::kSoftWarps); // the next P goes there
       }
       tc_fence_before();
       named_bar_sync(bar, 128);                      // the sums have been read
