@@ -140,15 +140,21 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Two floats to e5m2 (round to nearest even, saturating), low byte first; its
-// code is the upper byte of the fp16 of the same value.
-__device__ __forceinline__ uint32_t to_e5m2x2(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
-}
-
-__device__ __forceinline__ float2 from_e5m2x2(uint32_t codes) {
-  const uint32_t h = __byte_perm(codes, 0, 0x1404);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// Four nonnegative floats below 2^15.9 as sums of two e5m2 terms, a byte each. An
+// e5m2 code is the upper byte of the fp16 of its value, so the first term is
+// the fp16 rounded to its upper byte, and what is left over, exact in fp16, is
+// rounded the same way (halves away from zero). In integer operations: the
+// conversions to 8 bits run at an eighth of their rate. A NaN is lost here.
+__device__ __forceinline__ void split_e5m2x4(float p0, float p1, float p2, float p3, uint32_t& hi,
+                                             uint32_t& lo) {
+  const __half2 a = __floats2half2_rn(p0, p1), b = __floats2half2_rn(p2, p3);
+  const uint32_t ua = (*reinterpret_cast<const uint32_t*>(&a) + 0x00800080u) & 0xff00ff00u;
+  const uint32_t ub = (*reinterpret_cast<const uint32_t*>(&b) + 0x00800080u) & 0xff00ff00u;
+  const __half2 ra = __hsub2(a, *reinterpret_cast<const __half2*>(&ua));
+  const __half2 rb = __hsub2(b, *reinterpret_cast<const __half2*>(&ub));
+  hi = __byte_perm(ua, ub, 0x7531);
+  lo = __byte_perm(*reinterpret_cast<const uint32_t*>(&ra) + 0x00800080u,
+                   *reinterpret_cast<const uint32_t*>(&rb) + 0x00800080u, 0x7531);
 }
 
 // Sums v[i] over the 32 lanes; lane l gets the sum of element l % N. The order
@@ -265,8 +271,45 @@ __device__ __forceinline__ Kv8Range kv8_range(const KeySide& ks, bool sparse, in
 // are as exact as the codes themselves. Four 128-byte-swizzled chunks of 128
 // columns, 2 ROWS rows each, then the rope columns in 64-byte rows.
 // Returns through set(h, s) the exponent of each head. An infinity or NaN makes
-// the whole head NaN. Warp `warp` of WARPS takes heads warp, warp + WARPS, ...
-// Up to four heads are fetched at a time, before any of them is converted.
+// the whole head NaN. Warp `warp` of WARPS takes ROWS / WARPS heads in a row.
+// Each warp fetches its heads (up to four at a time) with 16-byte loads: two for
+// the latent columns of a head, and one for the rope columns of four heads.
+struct Q8Pieces {
+  uint32_t hi[2], lo[2];                            // 8 codes of each term
+};
+
+// 8 bf16 times f = 2^(-s - 8). The fp16 of 2^-8 times a value has that value's
+// e4m3 code in bits 7 to 14, below the sign.
+__device__ __forceinline__ Q8Pieces split_q8(uint4 v, float f, bool bad) {
+  const __half2 k4096 = __float2half2_rn(4096.f);   // 2^8 back, 16 of the second term
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  Q8Pieces r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const __half2 x = __floats2half2_rn(__uint_as_float(w[2 * i + j] << 16) * f,
+                                          __uint_as_float(w[2 * i + j] & 0xffff0000u) * f);
+      const uint32_t u = (*reinterpret_cast<const uint32_t*>(&x) + 0x00400040u) & 0xff80ff80u;
+      const __half2 rest = __hsub2(x, *reinterpret_cast<const __half2*>(&u));
+      h[j] = ((u << 1) & 0x7f007f00u) | (u & 0x80008000u);
+      l[j] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hmul2(rest, k4096)), __NV_SATFINITE,
+                                        __NV_E4M3);
+    }
+    r.hi[i] = bad ? 0x7f7f7f7fu : __byte_perm(h[0], h[1], 0x7531);
+    r.lo[i] = bad ? 0x7f7f7f7fu : l[0] | (l[1] << 16);
+  }
+  return r;
+}
+
+__device__ __forceinline__ uint32_t bf16_amax(uint4 v) {   // as bits
+  const uint32_t a = __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu);
+  const uint32_t b = __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
+  const uint32_t c = __vmaxu2(a, b);
+  return max(c & 0xffffu, c >> 16);
+}
+
 template <int ROWS, int WARPS, typename F>
 __device__ __forceinline__ void stage_q8(uint8_t* tile, const __nv_bfloat16* q, int live, int warp,
                                          int lane, F set) {
@@ -275,45 +318,50 @@ __device__ __forceinline__ void stage_q8(uint8_t* tile, const __nv_bfloat16* q, 
   static_assert(ROWS % WARPS == 0 && kPerWarp % kBatch == 0, "");
 #pragma unroll 1
   for (int r0 = 0; r0 < kPerWarp; r0 += kBatch) {
-    uint32_t w[kBatch][9];
+    const int h0 = warp * kPerWarp + r0;            // heads h0 .. h0 + kBatch - 1
+    const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h0) * kRow8);
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    uint4 v[kBatch][2];
 #pragma unroll
     for (int r = 0; r < kBatch; ++r) {
-      const int h = warp + WARPS * (r0 + r);
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(h) * kRow8);
-#pragma unroll
-      for (int i = 0; i < 9; ++i) w[r][i] = h < live ? __ldg(src + lane + 32 * i) : 0u;
+      v[r][0] = h0 + r < live ? __ldg(src + 72 * r + lane) : none;
+      v[r][1] = h0 + r < live ? __ldg(src + 72 * r + 32 + lane) : none;
     }
+    const int rr = lane >> 3;                       // the head whose rope columns this lane takes
+    const uint4 vr = rr < kBatch && h0 + rr < live ? __ldg(src + 72 * rr + 64 + (lane & 7)) : none;
+    uint32_t mr = bf16_amax(vr);
+#pragma unroll
+    for (int off = 4; off >= 1; off >>= 1) mr = max(mr, __shfl_xor_sync(0xffffffffu, mr, off));
+    float f_mine = 0.f;                             // of head rr
+    bool bad_mine = false;
 #pragma unroll
     for (int r = 0; r < kBatch; ++r) {
-      const int h = warp + WARPS * (r0 + r);
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 9; ++i) m = max(m, max(w[r][i] & 0x7fffu, (w[r][i] >> 16) & 0x7fffu));
-      m = __reduce_max_sync(0xffffffffu, m);
+      const int h = h0 + r;
+      const uint32_t m = max(__reduce_max_sync(0xffffffffu, max(bf16_amax(v[r][0]), bf16_amax(v[r][1]))),
+                             __shfl_sync(0xffffffffu, mr, 8 * r));
       const bool bad = m >= 0x7f80u;
-      const int s = min(max(static_cast<int>(m >> 7) - 127 - 7, -120), 120);
-      const float f = pow2i(-s);
-#pragma unroll
-      for (int i = 0; i < 9; ++i) {
-        const float x = __uint_as_float(w[r][i] << 16) * f, y = __uint_as_float(w[r][i] & 0xffff0000u) * f;
-        uint32_t hi = to_e4m3x2(x, y);
-        const float2 b = from_e4m3x2(hi);
-        uint32_t lo = to_e4m3x2((x - b.x) * 16.f, (y - b.y) * 16.f);
-        if (bad) hi = lo = 0x7f7fu;
-        const int col = 2 * (lane + 32 * i);
-        uint8_t* at;
-        int step;                                   // from the first term's row to the second's
-        if (i < 8) {
-          at = tile + (col >> 7) * kChunk + h * 128 + ((((col & 127) >> 4) ^ (h & 7)) << 4);
-          step = ROWS * 128;
-        } else {
-          at = tile + 4 * kChunk + h * 64 + ((((col - 512) >> 4) ^ ((h >> 1) & 3)) << 4);
-          step = ROWS * 64;
-        }
-        *reinterpret_cast<uint16_t*>(at + (col & 15)) = static_cast<uint16_t>(hi);
-        *reinterpret_cast<uint16_t*>(at + step + (col & 15)) = static_cast<uint16_t>(lo);
+      const int s = min(max(static_cast<int>(m >> 7) - 127 - 7, -112), 120);
+      const float f = pow2i(-s - 8);
+      if (rr == r) {
+        f_mine = f;
+        bad_mine = bad;
       }
       if (lane == 0) set(h, s);
+      // lane's 8 columns 8 lane (+ 256): chunk lane / 16 (+ 2), 8-byte half of a 16-byte unit
+      uint8_t* const at = tile + (lane >> 4) * kChunk + h * 128 + ((((lane & 15) >> 1) ^ (h & 7)) << 4) + 8 * (lane & 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const Q8Pieces c = split_q8(v[r][i], f, bad);
+        *reinterpret_cast<uint2*>(at + 2 * i * kChunk) = make_uint2(c.hi[0], c.hi[1]);
+        *reinterpret_cast<uint2*>(at + 2 * i * kChunk + ROWS * 128) = make_uint2(c.lo[0], c.lo[1]);
+      }
+    }
+    if (rr < kBatch) {
+      const int h = h0 + rr;
+      const Q8Pieces c = split_q8(vr, f_mine, bad_mine);
+      uint8_t* const at = tile + 4 * kChunk + h * 64 + ((((lane & 7) >> 1) ^ ((h >> 1) & 3)) << 4) + 8 * (lane & 1);
+      *reinterpret_cast<uint2*>(at) = make_uint2(c.hi[0], c.hi[1]);
+      *reinterpret_cast<uint2*>(at + ROWS * 64) = make_uint2(c.lo[0], c.lo[1]);
     }
   }
 }

@@ -351,10 +351,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
               p[t] = ex2(x);
               pl[i + t] = p[t];
             }
-            const uint32_t h0 = to_e5m2x2(p[0], p[1]), h1 = to_e5m2x2(p[2], p[3]);
-            const float2 b0 = from_e5m2x2(h0), b1 = from_e5m2x2(h1);
-            hi[i / 4] = h0 | (h1 << 16);
-            lo[i / 4] = to_e5m2x2(p[0] - b0.x, p[1] - b0.y) | (to_e5m2x2(p[2] - b1.x, p[3] - b1.y) << 16);
+            split_e5m2x4(p[0], p[1], p[2], p[3], hi[i / 4], lo[i / 4]);
           }
           const bool again = !add && named_bar_any(bar, 128, over);
           if (!again)
@@ -455,30 +452,32 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
             if (hb + t < live) dst[t * 512] = __uint_as_float(o[t]);
         }
       } else {
-        // rows of 128 columns go through the P tile (its last reader is done), so
-        // that a warp stores whole lines instead of 64 bytes of each head
-        __nv_bfloat16* const buf = reinterpret_cast<__nv_bfloat16*>(S.p) + hb * 128;
-        const int t4 = threadIdx.x & 127;
-        __nv_bfloat16* const out = a.out + (static_cast<int64_t>(done.qi) * a.heads + head0 + hb) * 512;
+        // each warp turns its 32 columns x HN heads in a corner of the P tile (whose
+        // last reader is done), so that a lane stores 16 bytes of one head
+        __nv_bfloat16* const buf = reinterpret_cast<__nv_bfloat16*>(S.p) + warp * (32 * HN);
+        __nv_bfloat16* const out =
+            a.out + (static_cast<int64_t>(done.qi) * a.heads + head0 + hb) * 512 + 32 * sub;
+        float f[HN];
+#pragma unroll
+        for (int t = 0; t < HN; ++t) f[t] = __shfl_sync(0xffffffffu, inv, t);
+        uint32_t o[HN];
+        tmem_ld<HN>(t_lane + hb, o);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          uint32_t o[HN];
-          tmem_ld<HN>(t_lane + c * NP + hb, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int t = 0; t < HN; ++t) {
-            const float f = __shfl_sync(0xffffffffu, inv, t);
-            buf[t * 128 + 32 * sub + lane] = __float2bfloat16(f == 0.f ? 0.f : __uint_as_float(o[t]) * f);
-          }
-          named_bar_sync(bar, 128);
+          for (int t = 0; t < HN; ++t)
+            buf[t * 32 + lane] = __float2bfloat16(__uint_as_float(o[t]) * f[t]);
+          if (c < 3) tmem_ld<HN>(t_lane + (c + 1) * NP + hb, o);
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < HN / 8; ++i) {
-            const int t = 8 * i + (t4 >> 4);
+            const int t = 8 * i + (lane >> 2);
             if (hb + t < live)
-              *reinterpret_cast<uint4*>(out + t * 512 + c * 128 + 8 * (t4 & 15)) =
-                  *reinterpret_cast<const uint4*>(buf + t * 128 + 8 * (t4 & 15));
+              *reinterpret_cast<uint4*>(out + t * 512 + c * 128 + 8 * (lane & 3)) =
+                  *reinterpret_cast<const uint4*>(buf + t * 32 + 8 * (lane & 3));
           }
-          named_bar_sync(bar, 128);
+          __syncwarp();
         }
         named_bar_sync(kBarAll, 32 * C::kSoftWarps); // the next P goes there
       }
