@@ -140,14 +140,39 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Four nonnegative floats below 2^15.9 as sums of two e5m2 terms, a byte each. An
+// Two fp32 lanes in one instruction.
+__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2_unpack(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Four nonnegative fp16 values as sums of two e5m2 terms, a byte each. An
 // e5m2 code is the upper byte of the fp16 of its value, so the first term is
-// the fp16 rounded to its upper byte, and what is left over, exact in fp16, is
+// the value rounded to its upper byte, and what is left over, exact in fp16, is
 // rounded the same way (halves away from zero). In integer operations: the
 // conversions to 8 bits run at an eighth of their rate. A NaN is lost here.
-__device__ __forceinline__ void split_e5m2x4(float p0, float p1, float p2, float p3, uint32_t& hi,
-                                             uint32_t& lo) {
-  const __half2 a = __floats2half2_rn(p0, p1), b = __floats2half2_rn(p2, p3);
+__device__ __forceinline__ void split_e5m2x4(__half2 a, __half2 b, uint32_t& hi, uint32_t& lo) {
   const uint32_t ua = (*reinterpret_cast<const uint32_t*>(&a) + 0x00800080u) & 0xff00ff00u;
   const uint32_t ub = (*reinterpret_cast<const uint32_t*>(&b) + 0x00800080u) & 0xff00ff00u;
   const __half2 ra = __hsub2(a, *reinterpret_cast<const __half2*>(&ua));
@@ -263,7 +288,7 @@ __device__ __forceinline__ Kv8Range kv8_range(const KeySide& ks, bool sparse, in
 
 // ------------------------------------------------------------------ queries as two e4m3 terms
 
-// Writes the queries of `rows` heads (of which `live` exist) as B operands: row
+// Writes the queries of ROWS heads (of which `live` exist) as the image of a B operand: row
 // h of the tiles is e4m3(q 2^-s), row ROWS + h is e4m3 of 16 times what that left
 // over, with s per head so that the largest element lies in [128, 256). The two
 // terms hold a bf16 element exactly down to 2^-14 of the head's largest one and
@@ -366,11 +391,35 @@ __device__ __forceinline__ void stage_q8(uint8_t* tile, const __nv_bfloat16* q, 
   }
 }
 
-// Fetches `live` heads of a query into L2 (for stage_q8), `lanes` threads sharing the lines.
-__device__ __forceinline__ void prefetch_q8(const __nv_bfloat16* q, int live, int lane, int lanes) {
-  const char* p = reinterpret_cast<const char*>(q);
-  for (int i = 128 * lane; i < live * kRow8 * 2; i += 128 * lanes)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
+// Bytes of one such image, and of a head group's scales behind it.
+template <int ROWS>
+constexpr int kQ8Bytes = 2 * ROWS * kRow8;
+
+// Copies `bytes` (a multiple of 16, both addresses 16-byte aligned) from global
+// into this CTA's shared memory, counted on `bar` (complete_tx).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// One query's head group per block: its operand image and, per head, the factor
+// that turns hi + lo / 16 into base-2 logits. This is a kernel of its own, before the
+// attention: there the conversion (~250 instructions a head and warp) stood
+// between one query and the next, 6700 cycles of every 64-head query.
+template <int ROWS, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS)
+kv8_q8_kernel(const __nv_bfloat16* q, int64_t ld_q, int heads, int groups, int group_heads,
+              float scale_log2, uint8_t* images, float* factors) {
+  griddep_launch_dependents();
+  const int64_t item = blockIdx.x;                  // query * groups + group
+  const int head0 = static_cast<int>(item % groups) * group_heads;
+  stage_q8<ROWS, WARPS>(images + item * kQ8Bytes<ROWS>,
+                        q + (item / groups) * ld_q + static_cast<int64_t>(head0) * kRow8,
+                        min(group_heads, heads - head0), threadIdx.x >> 5, threadIdx.x & 31,
+                        [&](int h, int s) { factors[item * ROWS + h] = scale_log2 * pow2i(s); });
 }
 
 }  // namespace dsa

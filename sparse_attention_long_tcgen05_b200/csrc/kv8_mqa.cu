@@ -42,8 +42,6 @@
 // issues the logits' MMAs, one that issues the values', and four that copy. (One
 // issuing warp that polled for whichever could go on was bound by its own
 // polling: 400 cycles a unit of 4 or 8 MMAs.)
-#include <cfloat>
-
 #include "kv8_gather.cuh"
 
 namespace dsa {
@@ -55,6 +53,7 @@ constexpr int kMaxWorkers = 148;
 // range (57344 = 1.75 * 2^15) is used to the top.
 constexpr float kRescale = 6.f;
 constexpr float kShift = 9.f;
+constexpr float kTop = 32768.f;      // 2^(kRescale + kShift)
 constexpr float kLn2 = 0.69314718055994531f;
 
 // NP: heads of a CTA, padded. The ring takes what shared memory is left by the
@@ -78,7 +77,8 @@ struct Smem {
   alignas(1024) uint8_t q[2 * NP * 576];
   alignas(1024) uint8_t p[kTile * 128];              // row = key: first terms at byte 0, second at 64
   Kv8Ring<Cfg<NP>::kRing, Cfg<NP>::kMeta> ring;
-  alignas(16) float head_scale[NP];                  // logit2 = (hi + lo / 16) * 2^e * head_scale
+  alignas(16) float head_scale[NP];                  // logit2 = (hi + lo / 16) 2^e head_scale
+  alignas(16) float neg_ref[NP];                     // kShift - running maximum
   uint64_t q_full, p_full, pv_done, drained;
   uint64_t s_full[2], s_empty[2];
   uint32_t tmem_base;
@@ -96,20 +96,30 @@ struct Partials {
   int32_t* tail_item;       // [workers] query that begins here and is cut by the end, or -1
   float2* ml;               // [2 workers][heads] running maximum, sum
   float* o;                 // [2 workers][heads][512]
+  uint8_t* images;          // [n_q][groups] query operands (kv8_q8_kernel)
+  float* factors;           // [n_q][groups][NP]
 };
 
-__host__ __device__ inline size_t partials_bytes(int workers, int heads) {
-  return 2048 + static_cast<size_t>(2) * workers * heads * (sizeof(float2) + 512 * sizeof(float));
-}
+__host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-__host__ __device__ inline Partials partials(void* ws, int workers, int heads) {
-  Partials p;
-  p.head_item = static_cast<int32_t*>(ws);
-  p.head_goes_on = p.head_item + kMaxWorkers;
-  p.tail_item = p.head_goes_on + kMaxWorkers;
-  p.o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 2048);
-  p.ml = reinterpret_cast<float2*>(p.o + static_cast<size_t>(2) * workers * heads * 512);
-  return p;
+// Carves the workspace; returns its size. np: heads of a CTA, padded.
+__host__ __device__ inline size_t carve(void* ws, int workers, int heads, int64_t n_q, int groups, int np,
+                                        Partials* p) {
+  const size_t o_bytes = static_cast<size_t>(2) * workers * heads * 512 * sizeof(float);
+  const size_t ml_bytes = align256(static_cast<size_t>(2) * workers * heads * sizeof(float2));
+  const size_t image_bytes = static_cast<size_t>(n_q) * groups * 2 * np * kRow8;
+  const size_t factor_bytes = align256(static_cast<size_t>(n_q) * groups * np * sizeof(float));
+  if (p != nullptr) {
+    uint8_t* at = static_cast<uint8_t*>(ws);
+    p->head_item = reinterpret_cast<int32_t*>(at);
+    p->head_goes_on = p->head_item + kMaxWorkers;
+    p->tail_item = p->head_goes_on + kMaxWorkers;
+    p->o = reinterpret_cast<float*>(at += 2048);
+    p->ml = reinterpret_cast<float2*>(at += o_bytes);
+    p->images = at += ml_bytes;
+    p->factors = reinterpret_cast<float*>(at + image_bytes);
+  }
+  return 2048 + o_bytes + ml_bytes + image_bytes + factor_bytes;
 }
 static_assert(3 * kMaxWorkers * sizeof(int32_t) <= 2048, "");
 
@@ -139,7 +149,8 @@ struct Pieces {
 
 template <int NP>
 __global__ void __launch_bounds__(Cfg<NP>::kThreads, 1)
-kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_heads, int workers) {
+kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Partials part, int groups,
+               int group_heads, int workers) {
   using C = Cfg<NP>;
   using Ring = Kv8Ring<C::kRing, C::kMeta>;
   constexpr int R = C::kRing, HN = C::kHeads, kQkWarp = C::kSoftWarps, kPvWarp = kQkWarp + 1;
@@ -149,7 +160,6 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
   const int worker = blockIdx.x / groups, group = blockIdx.x % groups;
   const int head0 = group * group_heads;
   const int live = min(group_heads, a.heads - head0);
-  const Partials part = partials(a.ws, workers, a.heads);
   if (smem_u32(smem_raw) & 1023u) {                  // (never: nothing static lies before it)
     report(a.status, DSA_ERR_CUDA);
     return;
@@ -160,7 +170,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
   if (range.t0 == range.t1) return;
   if (threadIdx.x == 0) {
     S.ring.init();
-    mbar_init(&S.q_full, C::kSoftWarps);
+    mbar_init(&S.q_full, 1);
     mbar_init(&S.p_full, C::kSoftWarps);
     mbar_init(&S.pv_done, 1);
     mbar_init(&S.drained, 2);
@@ -174,6 +184,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_wait();                                    // the queries' operands
   const uint32_t tmem = S.tmem_base;
   Pieces pieces(a, range);
   Piece pc;
@@ -181,12 +192,8 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
   if (warp > kPvWarp) {
     // ------------------------------------------------------------ copies
     Kv8Gather<Ring> g{S.ring, S.slots, a, lane, warp - kPvWarp - 1};
-    while (pieces.next(pc)) {
-      if (pieces.left > 0)                           // the next query, for its staging
-        prefetch_q8(a.q + static_cast<int64_t>(pc.qi + 1) * a.ld_q + static_cast<int64_t>(head0) * kRow8,
-                    live, 32 * g.g + lane, 32 * kGatherWarps);
+    while (pieces.next(pc))
       if (!g.run(pc.qi, pc.j0, pc.n)) break;
-    }
     g.drain();
   } else if (warp == kQkWarp) {
     // ------------------------------------------------------------ S^T = K Q^T
@@ -198,6 +205,17 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
     uint32_t g = 0, slot = 0, phase = 0, n_piece = 0;
     bool ok = true;
     while (ok && pieces.next(pc)) {
+      // the operand of the query, once the last one's logits are all computed
+      if (g > 0) ok = mbar_wait_warp(&S.s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, a.status);
+      if (!ok) break;
+      if (elect_one()) {
+        const uint8_t* image = part.images + (static_cast<int64_t>(pc.qi) * groups + group) * kQ8Bytes<NP>;
+        mbar_arrive_expect_tx(&S.q_full, kQ8Bytes<NP>);
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c)
+          bulk_load(S.q + c * (kQ8Bytes<NP> / 8), image + c * (kQ8Bytes<NP> / 8), kQ8Bytes<NP> / 8, &S.q_full);
+      }
+      __syncwarp();
       ok = mbar_wait_warp(&S.q_full, n_piece & 1, a.status);
       ++n_piece;
       for (int j = 0; j < pc.n && ok; ++j, ++g) {
@@ -282,26 +300,26 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
     bool ok = true;
     bool more = pieces.next(pc);
 
-    auto stage_q = [&](const Piece& p) {
-      const __nv_bfloat16* q = a.q + static_cast<int64_t>(p.qi) * a.ld_q +
-                               static_cast<int64_t>(head0) * kRow8;
-      stage_q8<NP, C::kSoftWarps>(S.q, q, live, warp, lane,
-                   [&](int h, int s) { S.head_scale[h] = a.scale_log2 * pow2i(s); });
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.q_full);
-      named_bar_sync(kBarAll, 32 * C::kSoftWarps);   // head_scale is complete
+    // factor of head hb + lane % HN of a query
+    auto factor = [&](int qi) {
+      return __ldg(part.factors + (static_cast<int64_t>(qi) * groups + group) * NP + hb + lane % HN);
     };
-    stage_q(pc);
+    float next_factor = factor(pc.qi);
 
     // After a wait that ran out (reported) these warps go on without waiting: the
     // named barriers that they share are not bounded, so all of them must take
     // the same steps to the end.
     while (more) {
+      // (all four warps of these heads write the same values, after the barriers
+      // that end the last query)
+      const float* const hs = S.head_scale + hb;
+      if (lane < HN) S.head_scale[hb + lane] = next_factor;
+      __syncwarp();
+      if (pieces.left > 0) next_factor = factor(pc.qi + 1);
       float m_used = -INFINITY;                      // lane h % HN: running maximum of head hb + h
-      float l[HN];
+      uint64_t l[HN / 2];                            // this key's share of the sums, two heads a word
 #pragma unroll
-      for (int i = 0; i < HN; ++i) l[i] = 0.f;
+      for (int i = 0; i < HN / 2; ++i) l[i] = 0;
       for (int j = 0; j < pc.n; ++j, ++g) {
         const uint32_t b = g & 1;
         ok = ok && mbar_wait_warp(&S.ring.meta_full[g % C::kMeta], (g / C::kMeta) & 1, a.status) &&
@@ -309,8 +327,9 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
         tc_fence_after();
         const int e_key = S.ring.key_exp[g % C::kMeta][key];
         const bool valid = e_key != kNoKey;
-        const float ks = valid ? pow2i(e_key) : 0.f, e_add = valid ? static_cast<float>(e_key) : -INFINITY;
-        float y[HN];
+        const float ks = valid ? pow2i(e_key) : 0.f;
+        const uint64_t ks2 = f2_pack(ks, ks);
+        uint64_t s[HN / 2];                          // (hi + lo / 16) 2^e, two heads a word
         {
           uint32_t v[HN], w[HN];
           tmem_ld<HN>(t_lane + s_col + b * (2 * NP), v);
@@ -319,67 +338,88 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.s_empty[b]);
-          const float4* h4 = reinterpret_cast<const float4*>(S.head_scale + hb);
+          const uint64_t k16 = f2_pack(0.0625f, 0.0625f);
 #pragma unroll
-          for (int i = 0; i < HN; i += 4) {
-            const float4 f = h4[i / 4];
-            const float ff[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const float s = fmaf(__uint_as_float(w[i + t]), 0.0625f, __uint_as_float(v[i + t]));
-              y[i + t] = fmaf(s * ks, ff[t], e_add);
-            }
-          }
+          for (int i = 0; i < HN; i += 2)
+            s[i / 2] = f2_mul(f2_fma(f2_pack(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), k16,
+                                     f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1]))), ks2);
         }
-        // P' and its two terms, with the maximum as it stands; where that is more
-        // than 2^kRescale too low (in a query's first tile, and at a head's first
-        // key, always) it is found anew
-        uint32_t hi[HN / 4], lo[HN / 4];
-        const float inv_scale = valid ? pow2i(-e_key) : 0.f;
+        // 2^(z - M) for the sum and P' = 2^(z + e - M) in fp16, with the maximum as
+        // it stands; where that is more than 2^kRescale too low (in a query's first
+        // tile, and at a head's first key, always) it is found anew
+        const bool all_valid = __all_sync(0xffffffffu, valid);
+        uint64_t w[HN / 2];
+        __half2 p[HN / 2];
+        auto weigh = [&]() {
+          const ulonglong2* f4 = reinterpret_cast<const ulonglong2*>(hs);
+          const ulonglong2* r4 = reinterpret_cast<const ulonglong2*>(S.neg_ref + hb);
+#pragma unroll
+          for (int i = 0; i < HN / 2; i += 2) {
+            const ulonglong2 f = f4[i / 2], r = r4[i / 2];
+            w[i] = f2_fma(s[i], f.x, r.x);
+            w[i + 1] = f2_fma(s[i + 1], f.y, r.y);
+          }
+          if (!all_valid) {
+#pragma unroll
+            for (int i = 0; i < HN / 2; ++i)
+              if (!valid) w[i] = f2_pack(-INFINITY, -INFINITY);
+          }
+#pragma unroll
+          for (int i = 0; i < HN / 2; ++i) {
+            const float2 x = f2_unpack(w[i]);
+            w[i] = f2_pack(ex2(x.x), ex2(x.y));
+            const float2 y = f2_unpack(f2_mul(w[i], ks2));
+            p[i] = __floats2half2_rn(y.x, y.y);
+          }
+        };
         float alpha = 1.f;
         bool rescale = false;
-        auto weigh = [&](float ref, bool add) {
-          bool over = false;
-          float pl[HN];
+        bool fresh = j == 0;
+        if (!fresh) {
+          weigh();
+          __half2 top = p[0];
 #pragma unroll
-          for (int i = 0; i < HN; i += 4) {
-            float p[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const float x = y[i + t] - __shfl_sync(0xffffffffu, ref, i + t);
-              over |= x > kRescale + kShift;
-              p[t] = ex2(x);
-              pl[i + t] = p[t];
-            }
-            split_e5m2x4(p[0], p[1], p[2], p[3], hi[i / 4], lo[i / 4]);
-          }
-          const bool again = !add && named_bar_any(bar, 128, over);
-          if (!again)
-#pragma unroll
-            for (int i = 0; i < HN; ++i) l[i] = fmaf(pl[i], inv_scale, l[i]);
-          return again;
-        };
-        if (j == 0 || weigh(m_used == -INFINITY ? -FLT_MAX : m_used - kShift, false)) {
+          for (int i = 1; i < HN / 2; ++i) top = __hmax2(top, p[i]);
+          const float2 t2 = __half22float2(top);
+          fresh = named_bar_any(bar, 128, fmaxf(t2.x, t2.y) > kTop);
+        }
+        if (fresh) {
           float mine = -INFINITY;
+          const float e_add = valid ? static_cast<float>(e_key) : -INFINITY;
 #pragma unroll
           for (int i = 0; i < HN; ++i) {
-            const float m = warp_max(y[i]);
+            const float2 x = f2_unpack(s[i / 2]);
+            const float m = warp_max(fmaf(i % 2 ? x.y : x.x, hs[i], e_add));
             if (lane % HN == i) mine = m;
           }
           if (lane < HN) S.tile_max[b][sub][hb + lane] = mine;
           named_bar_sync(bar, 128);
           float mx = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) mx = fmaxf(mx, S.tile_max[b][w][hb + lane % HN]);
-          const float m_next = mx > m_used ? mx : m_used;
-          alpha = mx > m_used ? ex2(m_used - m_next) : 1.f;
-          m_used = m_next;
+          for (int t = 0; t < 4; ++t) mx = fmaxf(mx, S.tile_max[b][t][hb + lane % HN]);
+          if (mx > m_used) {
+            alpha = ex2(m_used - mx);
+            m_used = mx;
+          }
           rescale = j > 0;
+          // (the four warps of these heads write the same values; without a key yet,
+          // one that the first key exceeds)
+          if (lane < HN) S.neg_ref[hb + lane] = m_used == -INFINITY ? 1e30f : kShift - m_used;
+          __syncwarp();
+          weigh();
           if (rescale) {
 #pragma unroll
-            for (int i = 0; i < HN; ++i) l[i] *= __shfl_sync(0xffffffffu, alpha, i);
+            for (int i = 0; i < HN; i += 2)
+              l[i / 2] = f2_mul(l[i / 2], f2_pack(__shfl_sync(0xffffffffu, alpha, i),
+                                                  __shfl_sync(0xffffffffu, alpha, i + 1)));
           }
-          weigh(m_next == -INFINITY ? 0.f : m_next - kShift, true);
+        }
+        uint32_t hi[HN / 4], lo[HN / 4];
+#pragma unroll
+        for (int i = 0; i < HN / 2; i += 2) {
+          l[i] = f2_add(l[i], w[i]);
+          l[i + 1] = f2_add(l[i + 1], w[i + 1]);
+          split_e5m2x4(p[i], p[i + 1], hi[i / 2], lo[i / 2]);
         }
         // the value products of the tile before are done: P and O may be written
         if (g > 0) ok = ok && mbar_wait_warp(&S.pv_done, (g - 1) & 1, a.status);
@@ -412,14 +452,18 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.p_full);
       }
-      // the next query's logits may start while this one's result is written out
       const Piece done = pc;
       more = pieces.next(pc);
-      named_bar_sync(kBarAll, 32 * C::kSoftWarps);   // head_scale and S.q have been used
-      if (more) stage_q(pc);
 
       // sums over the keys: lanes, then the four warps in order
-      const float lw = reduce_columns<HN>(l, lane);
+      float ls[HN];
+#pragma unroll
+      for (int i = 0; i < HN / 2; ++i) {
+        const float2 x = f2_unpack(l[i]);
+        ls[2 * i] = x.x;
+        ls[2 * i + 1] = x.y;
+      }
+      const float lw = reduce_columns<HN>(ls, lane);
       if (lane < HN) S.tile_max[g & 1][sub][hb + lane] = lw;
       named_bar_sync(bar, 128);
       const bool cut = done.n < done.tiles;
@@ -453,10 +497,12 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
         }
       } else {
         // each warp turns its 32 columns x HN heads in a corner of the P tile (whose
-        // last reader is done), so that a lane stores 16 bytes of one head
-        __nv_bfloat16* const buf = reinterpret_cast<__nv_bfloat16*>(S.p) + warp * (32 * HN);
+        // last reader is done): words of two heads go in, and a lane takes 8 columns
+        // of two heads out, 16 bytes a store
+        uint32_t* const buf = reinterpret_cast<uint32_t*>(S.p) + warp * (16 * HN);
         __nv_bfloat16* const out =
             a.out + (static_cast<int64_t>(done.qi) * a.heads + head0 + hb) * 512 + 32 * sub;
+        const int t2 = 2 * (lane >> 2), d8 = 8 * (lane & 3);
         float f[HN];
 #pragma unroll
         for (int t = 0; t < HN; ++t) f[t] = __shfl_sync(0xffffffffu, inv, t);
@@ -466,16 +512,25 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
         for (int c = 0; c < 4; ++c) {
           tmem_wait_ld();
 #pragma unroll
-          for (int t = 0; t < HN; ++t)
-            buf[t * 32 + lane] = __float2bfloat16(__uint_as_float(o[t]) * f[t]);
+          for (int t = 0; t < HN; t += 2) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[t]) * f[t],
+                                                           __uint_as_float(o[t + 1]) * f[t + 1]);
+            buf[t * 16 + lane] = *reinterpret_cast<const uint32_t*>(&v);
+          }
           if (c < 3) tmem_ld<HN>(t_lane + (c + 1) * NP + hb, o);
           __syncwarp();
-#pragma unroll
-          for (int i = 0; i < HN / 8; ++i) {
-            const int t = 8 * i + (lane >> 2);
-            if (hb + t < live)
-              *reinterpret_cast<uint4*>(out + t * 512 + c * 128 + 8 * (lane & 3)) =
-                  *reinterpret_cast<const uint4*>(buf + t * 32 + 8 * (lane & 3));
+          if (t2 < HN) {
+            const uint4 x = *reinterpret_cast<const uint4*>(buf + t2 * 16 + d8);
+            const uint4 y = *reinterpret_cast<const uint4*>(buf + t2 * 16 + d8 + 4);
+            __nv_bfloat16* const dst = out + t2 * 512 + c * 128 + d8;
+            if (hb + t2 < live)
+              *reinterpret_cast<uint4*>(dst) =
+                  make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.z, x.w, 0x5410),
+                             __byte_perm(y.x, y.y, 0x5410), __byte_perm(y.z, y.w, 0x5410));
+            if (hb + t2 + 1 < live)
+              *reinterpret_cast<uint4*>(dst + 512) =
+                  make_uint4(__byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x7632),
+                             __byte_perm(y.x, y.y, 0x7632), __byte_perm(y.z, y.w, 0x7632));
           }
           __syncwarp();
         }
@@ -504,9 +559,8 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, int groups, int group_head
 // Joins the pieces of each query that a range end cut. Block (w, h): the query
 // that begins in worker w's range and goes on, head h.
 __global__ void __launch_bounds__(128)
-kv8_join_kernel(const __grid_constant__ Kv8AttnArgs a, int workers) {
+kv8_join_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Partials part, int workers) {
   griddep_wait();
-  const Partials part = partials(a.ws, workers, a.heads);
   const int w = blockIdx.x, h = blockIdx.y;
   const int qi = part.tail_item[w];
   if (qi < 0) return;
@@ -545,7 +599,7 @@ kv8_join_kernel(const __grid_constant__ Kv8AttnArgs a, int workers) {
 }
 
 struct Split {
-  int groups, group_heads, workers;
+  int groups, group_heads, np, workers;
 };
 
 // Head groups of at most 64, and as many workers as the device holds, but no
@@ -554,28 +608,51 @@ Split split(int32_t n_q, int32_t heads, int64_t max_keys, int num_sms) {
   Split s;
   s.groups = (heads + 63) / 64;
   s.group_heads = (heads + s.groups - 1) / s.groups;
+  s.np = s.group_heads <= 16 ? 16 : s.group_heads <= 32 ? 32 : 64;
   const int64_t tiles = n_q * ((max_keys + kTile - 1) / kTile);
   const int64_t most = (num_sms < kMaxWorkers ? num_sms : kMaxWorkers) / s.groups;
   s.workers = static_cast<int>(tiles < most ? tiles : most);
   return s;
 }
 
+// A kernel that may start while the one before it on the stream still runs
+// (griddep_wait marks where it needs it).
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int NP>
-cudaError_t launch(const Kv8AttnArgs& a, const Split& s, cudaStream_t stream) {
+cudaError_t launch(const Kv8AttnArgs& a, const Split& s, const Partials& part, cudaStream_t stream) {
   const size_t smem = sizeof(Smem<NP>);
   static_assert(sizeof(Smem<NP>) <= 232448, "shared memory of one CTA");
   cudaError_t e = cudaFuncSetAttribute(kv8_mqa_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  kv8_mqa_kernel<NP><<<s.workers * s.groups, Cfg<NP>::kThreads, smem, stream>>>(a, s.groups, s.group_heads, s.workers);
-  return cudaGetLastError();
+  constexpr int kWarps = NP / 4;                     // four heads a warp
+  kv8_q8_kernel<NP, kWarps><<<a.keys.n_q * s.groups, 32 * kWarps, 0, stream>>>(
+      a.q, a.ld_q, a.heads, s.groups, s.group_heads, a.scale_log2, part.images, part.factors);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_dependent(kv8_mqa_kernel<NP>, dim3(s.workers * s.groups), Cfg<NP>::kThreads, smem, stream, a,
+                          part, s.groups, s.group_heads, s.workers);
 }
 
 }  // namespace
 
 size_t kv8_mqa_workspace(int32_t n_q, int32_t heads, int64_t max_keys) {
   const Split s = split(n_q, heads, max_keys, kMaxWorkers);
-  return (partials_bytes(s.workers, heads) + 255) & ~size_t(255);
+  return carve(nullptr, s.workers, heads, n_q, s.groups, s.np, nullptr);
 }
 
 cudaError_t launch_kv8_mqa(const Kv8AttnArgs& a, int num_sms, int* launches, cudaStream_t stream) {
@@ -583,21 +660,14 @@ cudaError_t launch_kv8_mqa(const Kv8AttnArgs& a, int num_sms, int* launches, cud
                            : a.keys.paged   ? static_cast<int64_t>(a.keys.max_pages) * 64
                                             : a.keys.n_keys;
   const Split s = split(a.keys.n_q, a.heads, max_keys, num_sms);
-  cudaError_t e = s.group_heads <= 16   ? launch<16>(a, s, stream)
-                  : s.group_heads <= 32 ? launch<32>(a, s, stream)
-                                        : launch<64>(a, s, stream);
+  Partials part;
+  carve(a.ws, s.workers, a.heads, a.keys.n_q, s.groups, s.np, &part);
+  cudaError_t e = s.np == 16   ? launch<16>(a, s, part, stream)
+                  : s.np == 32 ? launch<32>(a, s, part, stream)
+                               : launch<64>(a, s, part, stream);
   if (e != cudaSuccess) return e;
-  ++*launches;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(s.workers, a.heads);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv8_join_kernel, a, s.workers);
+  *launches += 2;
+  e = launch_dependent(kv8_join_kernel, dim3(s.workers, a.heads), 128, 0, stream, a, part, s.workers);
   if (e != cudaSuccess) return e;
   ++*launches;
   return cudaSuccess;
