@@ -17,7 +17,8 @@ LIB = os.path.join(HERE, "libdsa.so")
 SOURCES = ["dsa_api.cu", "indexer_fp8.cu", "topk.cu", "sparse_mqa_bf16.cu", "simt_f32.cu",
            "indexer_kl.cu", "sparse_mqa_bwd.cu", "kv8_store.cu", "kv8_mqa.cu", "kv8_weights.cu",
            "kv8_evict.cu"]
-HEADERS = ["dsa_common.cuh", "dsa_kernels.h", "indexer_epilogue.cuh", "kv8_common.cuh", "kv8_gather.cuh"]
+HEADERS = ["dsa_common.cuh", "dsa_kernels.h", "indexer_epilogue.cuh", "kv8_common.cuh", "kv8_gather.cuh",
+           "kv8_split.cuh"]
 
 
 def nvcc() -> str:

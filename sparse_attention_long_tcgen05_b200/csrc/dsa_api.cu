@@ -686,7 +686,7 @@ DSA_API dsa_status dsa_workspace_size(int32_t op, const dsa_indexer_in* indexer,
       const int64_t keys = kv8_max_keys(*attn, k);
       *bytes = op == DSA_OP_KV8_MQA
                    ? dsa::kv8_mqa_workspace(attn->n_q, attn->heads, keys)
-                   : round256(static_cast<size_t>(attn->n_q) * keys * sizeof(float));
+                   : dsa::kv8_accumulate_workspace(attn->n_q, attn->heads, keys);
       return DSA_OK;
     }
     default:
@@ -818,7 +818,7 @@ DSA_API dsa_status dsa_kv8_accumulate(const dsa_attn_in* in, const int8_t* kv_ex
     return DSA_ERR_INVALID_ARG;
   if (ld_acc < kv8_max_keys(*in, 0)) return DSA_ERR_INVALID_ARG;
   const int64_t cols = kv8_max_keys(*in, idx != nullptr ? k : 0);
-  const size_t need = round256(static_cast<size_t>(in->n_q) * cols * sizeof(float));
+  const size_t need = dsa::kv8_accumulate_workspace(in->n_q, in->heads, cols);
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < need)
     return DSA_ERR_WORKSPACE_TOO_SMALL;
   DeviceInfo* dev = nullptr;

@@ -240,13 +240,15 @@ cudaError_t launch_kv8_mqa(const Kv8AttnArgs& a, int num_sms, int* launches, cud
 struct Kv8WeightArgs {
   Kv8AttnArgs attn;         // out, lse and ws unused
   const float* lse;         // [n_q, heads]
-  float* w;                 // [n_q, n_cols] workspace: mean over the heads
+  float* w;                 // the workspace; [n_q, n_cols]: mean over the heads
   int32_t n_cols;           // k, or the keys of the longest query
   float decay;
   float* acc;               // [n_seq, ld_acc]
   int64_t ld_acc;
 };
 
+// Workspace bytes of launch_kv8_accumulate.
+size_t kv8_accumulate_workspace(int32_t n_q, int32_t heads, int64_t n_cols);
 cudaError_t launch_kv8_accumulate(const Kv8WeightArgs& a, int num_sms, int* launches,
                                   cudaStream_t stream);
 

@@ -43,17 +43,16 @@
 // issuing warp that polled for whichever could go on was bound by its own
 // polling: 400 cycles a unit of 4 or 8 MMAs.)
 #include "kv8_gather.cuh"
+#include "kv8_split.cuh"
 
 namespace dsa {
 namespace {
 
 constexpr int kMaxWorkers = 148;
-// P' is kept within [0, 2^(kRescale + kShift)]: the maximum M is only moved when a
-// tile exceeds it by 2^kRescale, and P' is scaled by 2^kShift so that e5m2's
-// range (57344 = 1.75 * 2^15) is used to the top.
-constexpr float kRescale = 6.f;
+// P' is scaled by 2^kShift and kept within [0, kTop], e5m2's largest binade: the
+// maximum M is only moved when a tile exceeds it by more than 2^6.
 constexpr float kShift = 9.f;
-constexpr float kTop = 32768.f;      // 2^(kRescale + kShift)
+constexpr float kTop = 32768.f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 // NP: heads of a CTA, padded. The ring takes what shared memory is left by the
@@ -100,10 +99,8 @@ struct Partials {
   float* factors;           // [n_q][groups][NP]
 };
 
-__host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 // Carves the workspace; returns its size. np: heads of a CTA, padded.
-__host__ __device__ inline size_t carve(void* ws, int workers, int heads, int64_t n_q, int groups, int np,
+inline size_t carve(void* ws, int workers, int heads, int64_t n_q, int groups, int np,
                                         Partials* p) {
   const size_t o_bytes = static_cast<size_t>(2) * workers * heads * 512 * sizeof(float);
   const size_t ml_bytes = align256(static_cast<size_t>(2) * workers * heads * sizeof(float2));
@@ -122,30 +119,6 @@ __host__ __device__ inline size_t carve(void* ws, int workers, int heads, int64_
   return 2048 + o_bytes + ml_bytes + image_bytes + factor_bytes;
 }
 static_assert(3 * kMaxWorkers * sizeof(int32_t) <= 2048, "");
-
-// One query's part of a worker's range.
-struct Piece {
-  int qi, j0, n, tiles;     // tiles [j0, j0 + n) of the query's `tiles`
-};
-
-struct Pieces {
-  const Kv8AttnArgs& a;
-  int64_t left;
-  int qi, j0;
-  __device__ Pieces(const Kv8AttnArgs& args, const Kv8Range& r)
-      : a(args), left(r.t1 - r.t0), qi(r.qi), j0(r.j0) {}
-  __device__ __forceinline__ bool next(Piece& p) {
-    if (left <= 0) return false;
-    p.qi = qi;
-    p.j0 = j0;
-    p.tiles = kv8_tiles(a.keys, a.idx != nullptr, a.k, qi);
-    p.n = static_cast<int>(min(left, static_cast<int64_t>(p.tiles - j0)));
-    left -= p.n;
-    ++qi;
-    j0 = 0;
-    return true;
-  }
-};
 
 template <int NP>
 __global__ void __launch_bounds__(Cfg<NP>::kThreads, 1)
@@ -186,8 +159,8 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
   tc_fence_after();
   griddep_wait();                                    // the queries' operands
   const uint32_t tmem = S.tmem_base;
-  Pieces pieces(a, range);
-  Piece pc;
+  Kv8Pieces pieces(a, range);
+  Kv8Piece pc;
 
   if (warp > kPvWarp) {
     // ------------------------------------------------------------ copies
@@ -197,58 +170,8 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
     g.drain();
   } else if (warp == kQkWarp) {
     // ------------------------------------------------------------ S^T = K Q^T
-    constexpr uint32_t idesc = make_idesc(2 * NP, 0, 0, 0, 0);
-    const uint64_t q_desc = sw128_desc(smem_u32(S.q), 16, 1024);
-    const uint64_t qr_desc = sw64_desc(smem_u32(S.q) + 4 * (2 * NP * 128));
-    const uint64_t k_desc = sw128_desc(smem_u32(S.slots.chunk[0]), 16384, 1024);
-    const uint64_t r_desc = sw64_desc(smem_u32(S.slots.rope));
-    uint32_t g = 0, slot = 0, phase = 0, n_piece = 0;
-    bool ok = true;
-    while (ok && pieces.next(pc)) {
-      // the operand of the query, once the last one's logits are all computed
-      if (g > 0) ok = mbar_wait_warp(&S.s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, a.status);
-      if (!ok) break;
-      if (elect_one()) {
-        const uint8_t* image = part.images + (static_cast<int64_t>(pc.qi) * groups + group) * kQ8Bytes<NP>;
-        mbar_arrive_expect_tx(&S.q_full, kQ8Bytes<NP>);
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c)
-          bulk_load(S.q + c * (kQ8Bytes<NP> / 8), image + c * (kQ8Bytes<NP> / 8), kQ8Bytes<NP> / 8, &S.q_full);
-      }
-      __syncwarp();
-      ok = mbar_wait_warp(&S.q_full, n_piece & 1, a.status);
-      ++n_piece;
-      for (int j = 0; j < pc.n && ok; ++j, ++g) {
-        const uint32_t d = tmem + C::kColS + (g & 1) * (2 * NP);
-        ok = mbar_wait_warp(&S.s_empty[g & 1], ((g >> 1) & 1) ^ 1, a.status);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          ok = ok && mbar_wait_warp(&S.ring.full[slot], phase, a.status);
-          fence_proxy_async_smem();                  // the copies, before the MMAs read them
-          tc_fence_after();
-          const uint64_t kd = k_desc + slot * (kChunkB / 16), qd = q_desc + c * (2 * NP * 128 / 16);
-          if (ok && elect_one()) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f8(d, kd + 2 * k, qd + 2 * k, idesc, (c | k) != 0);
-          }
-          __syncwarp();
-          if (++slot == R) {
-            slot = 0;
-            phase ^= 1;
-          }
-        }
-        ok = ok && mbar_wait_warp(&S.ring.rope_full, g & 1, a.status);
-        fence_proxy_async_smem();
-        tc_fence_after();
-        if (ok && elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) mma_f8(d, r_desc + 2 * k, qr_desc + 2 * k, idesc, 1);
-          mma_commit(&S.s_full[g & 1]);
-          mma_commit(&S.ring.rope_empty);
-        }
-        __syncwarp();
-      }
-    }
+    kv8_logits<NP, R>(a, pieces, S.slots, S.ring, S.q, part.images, groups, group, &S.q_full, S.s_full, S.s_empty,
+                      tmem + C::kColS, lane, [](uint32_t) {});
     // nothing is in flight when the block ends, whichever way it got here
     if (elect_one()) mma_commit(&S.drained);
     __syncwarp();
@@ -345,7 +268,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
                                      f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1]))), ks2);
         }
         // 2^(z - M) for the sum and P' = 2^(z + e - M) in fp16, with the maximum as
-        // it stands; where that is more than 2^kRescale too low (in a query's first
+        // it stands; where P' is over kTop by it (in a query's first
         // tile, and at a head's first key, always) it is found anew
         const bool all_valid = __all_sync(0xffffffffu, valid);
         uint64_t w[HN / 2];
@@ -452,7 +375,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.p_full);
       }
-      const Piece done = pc;
+      const Kv8Piece done = pc;
       more = pieces.next(pc);
 
       // sums over the keys: lanes, then the four warps in order
@@ -613,24 +536,6 @@ Split split(int32_t n_q, int32_t heads, int64_t max_keys, int num_sms) {
   const int64_t most = (num_sms < kMaxWorkers ? num_sms : kMaxWorkers) / s.groups;
   s.workers = static_cast<int>(tiles < most ? tiles : most);
   return s;
-}
-
-// A kernel that may start while the one before it on the stream still runs
-// (griddep_wait marks where it needs it).
-template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
-                             A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int NP>
