@@ -6,17 +6,21 @@
 // largest weight stay. Weights become 32-bit keys whose integer order is the
 // weights' order; three histogram passes over 11, 11 and 10 bits find the
 // smallest kept key and how many of the keys equal to it stay (the ones of
-// lowest position), and a last pass writes the kept positions in order.
+// lowest position), and a last pass writes the kept positions in order. A
+// cluster of eight CTAs shares a sequence, an eighth of its positions each, and
+// adds its histograms and counts through distributed shared memory. Weights of
+// exactly zero, which most tokens of a long sequence may have, are counted by
+// ballots: as atomics they would all go to one address.
 // Move (kv8_move_kernel): a CTA per new page copies its 64 rows; the page's
 // exponent is the largest of its rows' old ones, so codes move unchanged or
 // are scaled down by a power of two. Bound: HBM, every kept row read and
 // written once.
-#include "kv8_common.cuh"
+#include "kv8_split.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kKeepThreads = 1024;
+constexpr int kKeepThreads = 512, kKeepCtas = 8;
 constexpr int kMoveThreads = 256;
 
 // Larger weight, larger key; -0 = +0; NaN below every number.
@@ -26,104 +30,196 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kKeepThreads)
+__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Sum of v over the lanes before this one, and over the whole warp in `all`.
+__device__ __forceinline__ uint32_t warp_before(uint32_t v, int lane, uint32_t& all) {
+  uint32_t inc = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t up = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += up;
+  }
+  all = __shfl_sync(0xffffffffu, inc, 31);
+  return inc - v;
+}
+
+__global__ void __cluster_dims__(kKeepCtas, 1, 1) __launch_bounds__(kKeepThreads)
 kv8_keep_kernel(const __grid_constant__ Kv8EvictArgs a) {
-  __shared__ uint32_t hist[2048];
-  __shared__ uint32_t warp_n[2][kKeepThreads / 32];
-  __shared__ uint32_t s_prefix, s_left;
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ __align__(16) uint32_t hist[2048];
+  __shared__ uint32_t warp_sum[kKeepThreads / 32];
+  __shared__ uint32_t s_prefix, s_left, s_zero, s_count[2];
+  const int b = blockIdx.x / kKeepCtas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_ctarank());
+  griddep_launch_dependents();
   int n = a.c.ctx_lens[b];
   if (n < 0 || n > a.c.max_pages * 64) {
-    if (tid == 0) report(a.status, DSA_ERR_DEVICE_BOUNDS);
+    if (tid == 0 && rank == 0) report(a.status, DSA_ERR_DEVICE_BOUNDS);
     n = 0;
   }
-  __syncthreads();                                 // new_lens may be ctx_lens
-  if (tid == 0) a.new_lens[b] = min(n, a.budget);
-  int32_t* kept = a.kept + b * a.ld_kept;
-  float* acc_out = a.acc_out + b * a.ld_acc_out;
-  const float* acc = a.acc + b * a.ld_acc;
+  cluster_sync();                                  // new_lens may be ctx_lens
+  if (tid == 0 && rank == 0) a.new_lens[b] = min(n, a.budget);
+  int32_t* const kept = a.kept + b * a.ld_kept;
+  float* const acc_out = a.acc_out + b * a.ld_acc_out;
+  const float* const acc = a.acc + b * a.ld_acc;
   const int mid = a.budget - a.sink - a.recent;    // kept between sink and recent
+  const int first = rank * kKeepThreads + tid, step = kKeepCtas * kKeepThreads;
   if (n <= a.budget) {
-    for (int i = tid; i < a.budget; i += kKeepThreads) {
+    for (int i = first; i < a.budget; i += step) {
       kept[i] = i < n ? i : -1;
       if (i < n) acc_out[i] = acc[i];
     }
     return;
   }
-  const int lo = a.sink, hi = n - a.recent;
-  for (int i = tid; i < a.sink + a.recent; i += kKeepThreads) {
+  for (int i = first; i < a.sink + a.recent; i += step) {
     const int at = i < a.sink ? i : i + mid;
     const int src = i < a.sink ? i : n - a.recent + (i - a.sink);
     kept[at] = src;
     acc_out[at] = acc[src];
   }
   if (mid == 0) return;
+  // this CTA's positions [lo, hi)
+  const int per = (n - a.recent - a.sink + kKeepCtas - 1) / kKeepCtas;
+  const int lo = min(a.sink + rank * per, n - a.recent), hi = min(lo + per, n - a.recent);
+  const uint32_t hist_addr = smem_u32(hist), count_addr = smem_u32(s_count);
+
   // the mid-th largest key, 11 + 11 + 10 bits from the top
   uint32_t prefix = 0, left = mid;
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const int bits = pass == 2 ? 10 : 11;
     for (int i = tid; i < 2048; i += kKeepThreads) hist[i] = 0;
+    if (tid == 0) s_zero = 0;
     __syncthreads();
-    for (int i = lo + tid; i < hi; i += kKeepThreads) {
-      const uint32_t key = weight_key(acc[i]);
-      if (pass == 0 || (key >> (shift + bits)) == prefix)
-        atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
+    uint32_t zeros = 0;
+    for (int i0 = lo; i0 < hi; i0 += kKeepThreads) {
+      const int i = i0 + tid;
+      const float x = i < hi ? acc[i] : 1.f;
+      zeros += x == 0.f;
+      if (i < hi && x != 0.f) {
+        const uint32_t key = weight_key(x);
+        if (pass == 0 || (key >> (shift + bits)) == prefix)
+          atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
+      }
     }
+    zeros = __reduce_add_sync(0xffffffffu, zeros);
+    if (lane == 0) atomicAdd(&s_zero, zeros);
     __syncthreads();
-    if (tid == 0) {                                // simple: walk down from the top bin
-      uint32_t sum = 0;
-      int d = (1 << bits) - 1;
-      while (sum + hist[d] < left) sum += hist[d--];
-      s_prefix = (prefix << bits) | static_cast<uint32_t>(d);
-      s_left = left - sum;
+    if (tid == 0) {
+      const uint32_t key = weight_key(0.f);
+      if (pass == 0 || (key >> (shift + bits)) == prefix) hist[(key >> shift) & ((1u << bits) - 1u)] += s_zero;
     }
+    cluster_sync();
+    // four bins a thread, summed over the cluster, the highest bins in thread 0
+    const int bin0 = 2044 - 4 * tid;
+    uint4 h = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int r = 0; r < kKeepCtas; ++r) {
+      const uint4 v = ld_cluster_v4(mapa_shared(hist_addr + 4 * bin0, r));
+      h.x += v.x;
+      h.y += v.y;
+      h.z += v.z;
+      h.w += v.w;
+    }
+    const uint32_t mine = h.x + h.y + h.z + h.w;
+    uint32_t all;
+    uint32_t before = warp_before(mine, lane, all);
+    if (lane == 0) warp_sum[warp] = all;
     __syncthreads();
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    if (before < left && left <= before + mine) {  // exactly one thread
+      const uint32_t c[4] = {h.w, h.z, h.y, h.x};
+      int d = 0;
+      while (before + c[d] < left) before += c[d++];
+      s_prefix = (prefix << bits) | static_cast<uint32_t>(bin0 + 3 - d);
+      s_left = left - before;
+    }
+    cluster_sync();                                // (also: the histograms have been read)
     prefix = s_prefix;
     left = s_left;
-    __syncthreads();
   }
-  // keys above the prefix stay, and the first `left` keys equal to it
+
+  // keys above the prefix stay, and the first `left` keys equal to it: how many of
+  // both lie before this CTA's positions
+  uint32_t n_gt = 0, n_eq = 0;
+  for (int i = lo + tid; i < hi; i += kKeepThreads) {
+    const uint32_t key = weight_key(acc[i]);
+    n_gt += key > prefix;
+    n_eq += key == prefix;
+  }
+  if (tid < 2) s_count[tid] = 0;
+  __syncthreads();
+  n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+  n_eq = __reduce_add_sync(0xffffffffu, n_eq);
+  if (lane == 0) {
+    atomicAdd(&s_count[0], n_gt);
+    atomicAdd(&s_count[1], n_eq);
+  }
+  cluster_sync();
   uint32_t base = 0, base_eq = 0;
-  for (int i0 = lo; i0 < hi; i0 += kKeepThreads) {
-    const int i = i0 + tid;
-    const float x = i < hi ? acc[i] : 0.f;
-    const uint32_t key = weight_key(x);
-    const bool gt = i < hi && key > prefix, eq = i < hi && key == prefix;
-    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) {
-      warp_n[0][warp] = __popc(bg);
-      warp_n[1][warp] = __popc(be);
-    }
-    __syncthreads();
-    uint32_t g = 0, e = 0, gt_all = 0, eq_all = 0;
-    for (int w = 0; w < kKeepThreads / 32; ++w) {
-      if (w == warp) {
-        g = gt_all;
-        e = eq_all;
-      }
-      gt_all += warp_n[0][w];
-      eq_all += warp_n[1][w];
-    }
-    const uint32_t below = (1u << lane) - 1u;
-    g += base + __popc(bg & below);
-    e += base_eq + __popc(be & below);
-    if (gt || (eq && e < left)) {
-      const uint32_t at = a.sink + g + min(e, left);
-      kept[at] = i;
-      acc_out[at] = x;
-    }
-    base += gt_all;
-    base_eq += eq_all;
-    __syncthreads();
+  for (int r = 0; r < rank; ++r) {
+    const uint32_t at = mapa_shared(count_addr, r);
+    base += ld_shared_cluster_u32(at);
+    base_eq += ld_shared_cluster_u32(at + 4);
   }
+  for (int i0 = lo; i0 < hi; i0 += 4 * kKeepThreads) {
+    float x[4];
+    uint32_t packed = 0, flags = 0;                // counts: above in the low half, equal in the high
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int i = i0 + 4 * tid + t;
+      x[t] = i < hi ? acc[i] : 0.f;
+      const uint32_t key = weight_key(x[t]);
+      if (i < hi && key > prefix) {
+        packed += 1u;
+        flags |= 1u << t;
+      } else if (i < hi && key == prefix) {
+        packed += 1u << 16;
+        flags |= 16u << t;
+      }
+    }
+    uint32_t all;
+    uint32_t before = warp_before(packed, lane, all);
+    __syncthreads();                               // warp_sum has been read
+    if (lane == 0) warp_sum[warp] = all;
+    __syncthreads();
+    uint32_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kKeepThreads / 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      total += warp_sum[w];
+    }
+    uint32_t g = base + (before & 0xffffu), e = base_eq + (before >> 16);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const bool gt = (flags >> t) & 1u, eq = (flags >> (4 + t)) & 1u;
+      if (gt || (eq && e < left)) {
+        const uint32_t at = a.sink + g + min(e, left);
+        kept[at] = i0 + 4 * tid + t;
+        acc_out[at] = x[t];
+      }
+      g += gt;
+      e += eq;
+    }
+    base += total & 0xffffu;
+    base_eq += total >> 16;
+  }
+  cluster_sync();                                  // no CTA leaves while its counts may be read
 }
 
 __global__ void __launch_bounds__(kMoveThreads)
 kv8_move_kernel(const __grid_constant__ Kv8EvictArgs a) {
   __shared__ int64_t s_row[64];
   __shared__ int s_exp[64];
-  const int b = blockIdx.y, page = blockIdx.x, tid = threadIdx.x;
+  const int b = blockIdx.x, page = blockIdx.y, tid = threadIdx.x;
+  griddep_wait();                                  // kept, new_lens
   const int m = min(64, a.new_lens[b] - page * 64);
   if (m <= 0) return;
   const int64_t to = a.dst_table[b * a.ld_dst + page];
@@ -148,19 +244,27 @@ kv8_move_kernel(const __grid_constant__ Kv8EvictArgs a) {
     s_exp[tid] = e;
   }
   __syncthreads();
-  int e = kExpMin;
-  for (int i = 0; i < m; ++i) e = max(e, s_exp[i]);
-  for (int i = tid; i < m * (kRow8 / 16); i += kMoveThreads) {
-    const int r = i / (kRow8 / 16), c = i % (kRow8 / 16);
-    if (s_row[r] < 0) continue;
-    uint4 x = *(reinterpret_cast<const uint4*>(a.c.codes + s_row[r] * a.c.ld) + c);
+  int e = max(s_exp[tid & 31], s_exp[32 + (tid & 31)]);   // (rows past m: the minimum)
+  e = __reduce_max_sync(0xffffffffu, e);
+  constexpr int kPieces = kRow8 / 16, kLoads = 64 * kPieces / kMoveThreads;
+  uint4 x[kLoads];                                 // all loads before the first store
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int u = tid + i * kMoveThreads, r = u / kPieces;
+    if (r < m && s_row[r] >= 0)
+      x[i] = *(reinterpret_cast<const uint4*>(a.c.codes + s_row[r] * a.c.ld) + u % kPieces);
+  }
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int u = tid + i * kMoveThreads, r = u / kPieces;
+    if (r >= m || s_row[r] < 0) continue;
     const int d = s_exp[r] - e;
     if (d != 0) {
       const float f = pow2i(max(d, -126));
-      x = make_uint4(rescale_e4m3x4(x.x, f), rescale_e4m3x4(x.y, f), rescale_e4m3x4(x.z, f),
-                     rescale_e4m3x4(x.w, f));
+      x[i] = make_uint4(rescale_e4m3x4(x[i].x, f), rescale_e4m3x4(x[i].y, f), rescale_e4m3x4(x[i].z, f),
+                        rescale_e4m3x4(x[i].w, f));
     }
-    *(reinterpret_cast<uint4*>(a.c.codes + (to * 64 + r) * a.c.ld) + c) = x;
+    *(reinterpret_cast<uint4*>(a.c.codes + (to * 64 + r) * a.c.ld) + u % kPieces) = x[i];
   }
   if (a.idx_codes != nullptr) {
     for (int i = tid; i < m * 8; i += kMoveThreads) {
@@ -177,12 +281,12 @@ kv8_move_kernel(const __grid_constant__ Kv8EvictArgs a) {
 }  // namespace
 
 cudaError_t launch_kv8_evict(const Kv8EvictArgs& a, int* launches, cudaStream_t stream) {
-  kv8_keep_kernel<<<a.c.n_seq, kKeepThreads, 0, stream>>>(a);
+  kv8_keep_kernel<<<kKeepCtas * a.c.n_seq, kKeepThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   ++*launches;
-  kv8_move_kernel<<<dim3((a.budget + 63) / 64, a.c.n_seq), kMoveThreads, 0, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_dependent(kv8_move_kernel, dim3(a.c.n_seq, (a.budget + 63) / 64), kMoveThreads, 0, stream, a);
+  if (e != cudaSuccess) return e;
   ++*launches;
   return cudaSuccess;
 }
