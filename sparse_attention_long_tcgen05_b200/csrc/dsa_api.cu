@@ -685,7 +685,7 @@ DSA_API dsa_status dsa_workspace_size(int32_t op, const dsa_indexer_in* indexer,
       DSA_TRY(check_kv8_attn(attn, &any_exp, k > 0 ? &any_idx : nullptr, k, k));
       const int64_t keys = kv8_max_keys(*attn, k);
       *bytes = op == DSA_OP_KV8_MQA
-                   ? dsa::kv8_mqa_workspace(attn->n_q, attn->heads, keys)
+                   ? dsa::kv8_mqa_workspace(attn->n_q, attn->heads, keys, k > 0)
                    : dsa::kv8_accumulate_workspace(attn->n_q, attn->heads, keys);
       return DSA_OK;
     }
@@ -794,7 +794,7 @@ DSA_API dsa_status dsa_kv8_mqa_fwd(const dsa_attn_in* in, const int8_t* kv_exp,
   DSA_TRY(check_kv8_attn(in, kv_exp, idx, ld_idx, k));
   if (out == nullptr || !aligned16(out)) return DSA_ERR_INVALID_ARG;
   const int64_t keys = kv8_max_keys(*in, idx != nullptr ? k : 0);
-  const size_t need = dsa::kv8_mqa_workspace(in->n_q, in->heads, keys);
+  const size_t need = dsa::kv8_mqa_workspace(in->n_q, in->heads, keys, idx != nullptr);
   if (need > 0 && (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < need))
     return DSA_ERR_WORKSPACE_TOO_SMALL;
   DeviceInfo* dev = nullptr;
@@ -804,7 +804,7 @@ DSA_API dsa_status dsa_kv8_mqa_fwd(const dsa_attn_in* in, const int8_t* kv_exp,
   a.lse = lse;
   a.ws = ws;
   return kv8_launched([&](int* n) {
-    return dsa::launch_kv8_mqa(a, dev->num_sms, n, reinterpret_cast<cudaStream_t>(stream));
+    return dsa::launch_kv8_mqa(a, n, reinterpret_cast<cudaStream_t>(stream));
   });
 }
 

@@ -234,8 +234,8 @@ struct Kv8AttnArgs {
 };
 
 // Workspace bytes of launch_kv8_mqa; max_keys: keys of the longest query.
-size_t kv8_mqa_workspace(int32_t n_q, int32_t heads, int64_t max_keys);
-cudaError_t launch_kv8_mqa(const Kv8AttnArgs& a, int num_sms, int* launches, cudaStream_t stream);
+size_t kv8_mqa_workspace(int32_t n_q, int32_t heads, int64_t max_keys, bool sparse);
+cudaError_t launch_kv8_mqa(const Kv8AttnArgs& a, int* launches, cudaStream_t stream);
 
 struct Kv8WeightArgs {
   Kv8AttnArgs attn;         // out, lse and ws unused

@@ -225,12 +225,19 @@ struct Kv8Range {
 };
 
 // Executed by the whole block (THREADS threads); scratch: THREADS / 32 + 2 words.
+// whole (selections only): ranges of whole queries instead.
 template <int THREADS>
 __device__ __forceinline__ Kv8Range kv8_range(const KeySide& ks, bool sparse, int k, int worker,
-                                              int workers, int64_t* scratch) {
+                                              int workers, bool whole, int64_t* scratch) {
   Kv8Range r{};
   if (sparse) {
     const int64_t per = (k + kTile - 1) / kTile, total = per * ks.n_q;
+    if (whole) {
+      r.qi = static_cast<int>(static_cast<int64_t>(ks.n_q) * worker / workers);
+      r.t0 = per * r.qi;
+      r.t1 = per * (static_cast<int64_t>(ks.n_q) * (worker + 1) / workers);
+      return r;
+    }
     r.t0 = total * worker / workers;
     r.t1 = total * (worker + 1) / workers;
     r.qi = static_cast<int>(r.t0 / per);

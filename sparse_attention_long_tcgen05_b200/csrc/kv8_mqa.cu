@@ -93,17 +93,17 @@ struct Partials {
   int32_t* head_item;       // [workers] query cut by the worker's beginning, or -1
   int32_t* head_goes_on;    // [workers] 1: that query is cut by its end as well
   int32_t* tail_item;       // [workers] query that begins here and is cut by the end, or -1
-  float2* ml;               // [2 workers][heads] running maximum, sum
-  float* o;                 // [2 workers][heads][512]
+  float2* ml;               // [2 workers][groups][NP] running maximum, sum
+  float* o;                 // [2 workers][groups][NP][512]
   uint8_t* images;          // [n_q][groups] query operands (kv8_q8_kernel)
   float* factors;           // [n_q][groups][NP]
 };
 
 // Carves the workspace; returns its size. np: heads of a CTA, padded.
-inline size_t carve(void* ws, int workers, int heads, int64_t n_q, int groups, int np,
-                                        Partials* p) {
-  const size_t o_bytes = static_cast<size_t>(2) * workers * heads * 512 * sizeof(float);
-  const size_t ml_bytes = align256(static_cast<size_t>(2) * workers * heads * sizeof(float2));
+inline size_t carve(void* ws, int workers, int64_t n_q, int groups, int np, Partials* p) {
+  const size_t rows = static_cast<size_t>(2) * workers * groups * np;
+  const size_t o_bytes = rows * 512 * sizeof(float);
+  const size_t ml_bytes = align256(rows * sizeof(float2));
   const size_t image_bytes = static_cast<size_t>(n_q) * groups * 2 * np * kRow8;
   const size_t factor_bytes = align256(static_cast<size_t>(n_q) * groups * np * sizeof(float));
   if (p != nullptr) {
@@ -123,7 +123,7 @@ static_assert(3 * kMaxWorkers * sizeof(int32_t) <= 2048, "");
 template <int NP>
 __global__ void __launch_bounds__(Cfg<NP>::kThreads, 1)
 kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Partials part, int groups,
-               int group_heads, int workers) {
+               int group_heads, int workers, bool whole) {
   using C = Cfg<NP>;
   using Ring = Kv8Ring<C::kRing, C::kMeta>;
   constexpr int R = C::kRing, HN = C::kHeads, kQkWarp = C::kSoftWarps, kPvWarp = kQkWarp + 1;
@@ -138,8 +138,8 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
     return;
   }
 
-  const Kv8Range range = kv8_range<C::kThreads>(a.keys, a.idx != nullptr, a.k, worker, workers, S.scratch);
-  if (threadIdx.x == 0 && group == 0) part.head_item[worker] = part.tail_item[worker] = -1;
+  const Kv8Range range = kv8_range<C::kThreads>(a.keys, a.idx != nullptr, a.k, worker, workers, whole, S.scratch);
+  if (threadIdx.x == 0 && group == 0 && !whole) part.head_item[worker] = part.tail_item[worker] = -1;
   if (range.t0 == range.t1) return;
   if (threadIdx.x == 0) {
     S.ring.init();
@@ -398,7 +398,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
       if (sub == 0 && lane < HN && hb + lane < live) {
         const int64_t h = head0 + hb + lane;
         if (cut)
-          part.ml[slot * a.heads + h] = make_float2(ref, lt);
+          part.ml[(slot * groups + group) * NP + hb + lane] = make_float2(ref, lt);
         else if (a.lse != nullptr)
           a.lse[static_cast<int64_t>(done.qi) * a.heads + h] =
               lt == 0.f ? -INFINITY : (ref + log2f(lt)) * kLn2;
@@ -413,10 +413,10 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
           uint32_t o[HN];
           tmem_ld<HN>(t_lane + c * NP + hb, o);
           tmem_wait_ld();
-          float* dst = part.o + (slot * a.heads + head0 + hb) * 512 + dim;
+          float* dst = part.o + ((slot * groups + group) * NP + hb) * 512 + dim;
 #pragma unroll
-          for (int t = 0; t < HN; ++t)
-            if (hb + t < live) dst[t * 512] = __uint_as_float(o[t]);
+          for (int i = 0; i < HN; ++i)
+            if (hb + i < live) dst[i * 512] = __uint_as_float(o[i]);
         }
       } else {
         // each warp turns its 32 columns x HN heads in a corner of the P tile (whose
@@ -479,62 +479,114 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
   }
 }
 
-// Joins the pieces of each query that a range end cut. Block (w, h): the query
-// that begins in worker w's range and goes on, head h.
-__global__ void __launch_bounds__(128)
-kv8_join_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Partials part, int workers) {
+// Joins the pieces of each query that a range end cut. Block (w, x): the query
+// that begins in worker w's range and goes on, four heads; its pieces are the last
+// of worker w, then the first of the next workers that have any tiles, up to the
+// one that does not go on. A thread takes four columns of a head, 128 a head.
+constexpr int kJoinThreads = 512;
+
+__global__ void __launch_bounds__(kJoinThreads, 4)
+kv8_join_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Partials part, int workers,
+                int groups, int group_heads, int np) {
+  __shared__ int32_t s_last;
+  __shared__ int s_base[kJoinThreads / 32];
+  __shared__ int16_t s_slot[kMaxWorkers];
+  __shared__ float s_f[4][kMaxWorkers];              // factor of a piece, per head
   griddep_wait();
-  const int w = blockIdx.x, h = blockIdx.y;
-  const int qi = part.tail_item[w];
+  const int w = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int qi = __ldcg(part.tail_item + w);
+  const int i = w + 1 + tid;                         // (workers <= 148 < the threads)
+  const bool mine = i < workers && __ldcg(part.head_item + i) == qi;
+  const bool ends = mine && __ldcg(part.head_goes_on + i) == 0;
   if (qi < 0) return;
-  // its pieces: the last of worker w, then the first of the next workers that
-  // have any tiles, up to the one that does not go on
-  float m = -INFINITY;
-  int last = workers - 1;
-  for (int i = w; i <= last; ++i) {
-    if (i > w && part.head_item[i] != qi) continue;
-    const float2 ml = part.ml[static_cast<int64_t>(2 * i + (i == w ? 1 : 0)) * a.heads + h];
-    if (ml.y != 0.f) m = fmaxf(m, ml.x);
-    if (i > w && part.head_goes_on[i] == 0) last = i;
+  if (ends) s_last = i;                              // one thread
+  __syncthreads();
+  const bool in = mine && i <= s_last;
+  const uint32_t votes = __ballot_sync(0xffffffffu, in);
+  if (lane == 0) s_base[warp] = __popc(votes);
+  __syncthreads();
+  int at = 1, n = 1;
+#pragma unroll
+  for (int x = 0; x < (kMaxWorkers + 31) / 32; ++x) {
+    if (x < warp) at += s_base[x];
+    n += s_base[x];
   }
-  float l = 0.f;
+  if (in) s_slot[at + __popc(votes & ((1u << lane) - 1u))] = static_cast<int16_t>(2 * i);
+  if (tid == 0) s_slot[0] = static_cast<int16_t>(2 * w + 1);
+  __syncthreads();
+  const int hq = warp >> 2;                          // this thread's head of the four
+  const int row = blockIdx.y * 4 + hq, group = row / np, h = row % np;   // (np is a multiple of 4)
+  const bool live = h < min(group_heads, a.heads - group * group_heads);
+  const int64_t head = static_cast<int64_t>(qi) * a.heads + group * group_heads + h;
+  if ((warp & 3) == 0 && live) {                     // the factors, a warp a head
+    float m = -INFINITY, l = 0.f;
+    for (int x = lane; x < n; x += 32) {
+      const float2 ml = __ldcg(part.ml + (static_cast<int64_t>(s_slot[x]) * groups + group) * np + h);
+      if (ml.y != 0.f) m = fmaxf(m, ml.x);
+    }
+    m = warp_max(m);
+    for (int x = lane; x < n; x += 32) {
+      const float2 ml = __ldcg(part.ml + (static_cast<int64_t>(s_slot[x]) * groups + group) * np + h);
+      const float f = ml.y != 0.f ? exp2f(ml.x - m) : 0.f;   // 0: no key of this piece counts
+      s_f[hq][x] = f;
+      l = fmaf(ml.y, f, l);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    if (lane == 0 && a.lse != nullptr) a.lse[head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __syncwarp();
+    for (int x = lane; x < n; x += 32) s_f[hq][x] *= inv;
+  }
+  __syncthreads();
+  if (!live) return;
+  const int d4 = tid & 127;
+  const int64_t stride = static_cast<int64_t>(groups) * np * 128;
+  const float4* src = reinterpret_cast<const float4*>(part.o) + (static_cast<int64_t>(group) * np + h) * 128 + d4;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = w; i <= last; ++i) {
-    if (i > w && part.head_item[i] != qi) continue;
-    const int64_t at = static_cast<int64_t>(2 * i + (i == w ? 1 : 0)) * a.heads + h;
-    const float2 ml = part.ml[at];
-    if (ml.y == 0.f) continue;                       // no key of this piece counts
-    const float f = exp2f(ml.x - m);
-    const float4 v = reinterpret_cast<const float4*>(part.o + at * 512)[threadIdx.x];
-    l = fmaf(ml.y, f, l);
-    o.x = fmaf(v.x, f, o.x);
-    o.y = fmaf(v.y, f, o.y);
-    o.z = fmaf(v.z, f, o.z);
-    o.w = fmaf(v.w, f, o.w);
+  for (int x0 = 0; x0 < n; x0 += 4) {
+    float4 v[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (x0 + x < n) v[x] = __ldcg(src + s_slot[x0 + x] * stride);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (x0 + x >= n) break;
+      const float f = s_f[hq][x0 + x];
+      o.x = fmaf(v[x].x, f, o.x);
+      o.y = fmaf(v[x].y, f, o.y);
+      o.z = fmaf(v[x].z, f, o.z);
+      o.w = fmaf(v[x].w, f, o.w);
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t out = static_cast<int64_t>(qi) * a.heads + h;
-  const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-  const __nv_bfloat162 y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  reinterpret_cast<uint2*>(a.out + out * 512)[threadIdx.x] =
+  const __nv_bfloat162 x = __floats2bfloat162_rn(o.x, o.y), y = __floats2bfloat162_rn(o.z, o.w);
+  reinterpret_cast<uint2*>(a.out + head * 512)[d4] =
       make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-  if (threadIdx.x == 0 && a.lse != nullptr) a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 struct Split {
   int groups, group_heads, np, workers;
+  bool whole;
 };
 
-// Head groups of at most 64, and as many workers as the device holds, but no
-// more than there can be tiles.
-Split split(int32_t n_q, int32_t heads, int64_t max_keys, int num_sms) {
+// Head groups of at most 64, and as many workers as a B200 holds, but no more than
+// there can be tiles. (A device with fewer SMs runs them in turn.)
+// A cut costs its worker an fp32 result and the call a joining kernel, as much as
+// about kCutTiles tiles. For selections, whose queries all have the same number of
+// tiles, the ranges are whole queries where that is no slower: 64 decode queries of
+// 16 tiles took 89 us cut for 74 workers and XX us whole on 64.
+constexpr int64_t kCutTiles = 6;
+
+Split split(int32_t n_q, int32_t heads, int64_t max_keys, bool sparse) {
   Split s;
   s.groups = (heads + 63) / 64;
   s.group_heads = (heads + s.groups - 1) / s.groups;
   s.np = s.group_heads <= 16 ? 16 : s.group_heads <= 32 ? 32 : 64;
-  const int64_t tiles = n_q * ((max_keys + kTile - 1) / kTile);
-  const int64_t most = (num_sms < kMaxWorkers ? num_sms : kMaxWorkers) / s.groups;
+  const int64_t per = (max_keys + kTile - 1) / kTile, tiles = n_q * per;
+  const int64_t most = kMaxWorkers / s.groups;
   s.workers = static_cast<int>(tiles < most ? tiles : most);
+  s.whole = sparse && (n_q + most - 1) / most * per <= (tiles + most - 1) / most + kCutTiles;
+  if (s.whole && n_q < s.workers) s.workers = n_q;
   return s;
 }
 
@@ -550,29 +602,31 @@ cudaError_t launch(const Kv8AttnArgs& a, const Split& s, const Partials& part, c
       a.q, a.ld_q, a.heads, s.groups, s.group_heads, a.scale_log2, part.images, part.factors);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_dependent(kv8_mqa_kernel<NP>, dim3(s.workers * s.groups), Cfg<NP>::kThreads, smem, stream, a,
-                          part, s.groups, s.group_heads, s.workers);
+                          part, s.groups, s.group_heads, s.workers, s.whole);
 }
 
 }  // namespace
 
-size_t kv8_mqa_workspace(int32_t n_q, int32_t heads, int64_t max_keys) {
-  const Split s = split(n_q, heads, max_keys, kMaxWorkers);
-  return carve(nullptr, s.workers, heads, n_q, s.groups, s.np, nullptr);
+size_t kv8_mqa_workspace(int32_t n_q, int32_t heads, int64_t max_keys, bool sparse) {
+  const Split s = split(n_q, heads, max_keys, sparse);
+  return carve(nullptr, s.whole ? 0 : s.workers, n_q, s.groups, s.np, nullptr);
 }
 
-cudaError_t launch_kv8_mqa(const Kv8AttnArgs& a, int num_sms, int* launches, cudaStream_t stream) {
+cudaError_t launch_kv8_mqa(const Kv8AttnArgs& a, int* launches, cudaStream_t stream) {
   const int64_t max_keys = a.idx != nullptr ? a.k
                            : a.keys.paged   ? static_cast<int64_t>(a.keys.max_pages) * 64
                                             : a.keys.n_keys;
-  const Split s = split(a.keys.n_q, a.heads, max_keys, num_sms);
+  const Split s = split(a.keys.n_q, a.heads, max_keys, a.idx != nullptr);
   Partials part;
-  carve(a.ws, s.workers, a.heads, a.keys.n_q, s.groups, s.np, &part);
+  carve(a.ws, s.whole ? 0 : s.workers, a.keys.n_q, s.groups, s.np, &part);
   cudaError_t e = s.np == 16   ? launch<16>(a, s, part, stream)
                   : s.np == 32 ? launch<32>(a, s, part, stream)
                                : launch<64>(a, s, part, stream);
   if (e != cudaSuccess) return e;
   *launches += 2;
-  e = launch_dependent(kv8_join_kernel, dim3(s.workers, a.heads), 128, 0, stream, a, part, s.workers);
+  if (s.whole) return cudaSuccess;
+  e = launch_dependent(kv8_join_kernel, dim3(s.workers, s.groups * s.np / 4), kJoinThreads, 0, stream, a, part,
+                       s.workers, s.groups, s.group_heads, s.np);
   if (e != cudaSuccess) return e;
   ++*launches;
   return cudaSuccess;

@@ -17,11 +17,12 @@
 namespace dsa {
 namespace {
 
-constexpr int kStoreThreads = 512;
-
+// Nine 16-byte pieces a thread: 512 threads for a bf16 block, two CTAs an SM, 1024
+// for an fp32 block.
 template <typename T>
-__global__ void __launch_bounds__(kStoreThreads)
+__global__ void __launch_bounds__(256 * sizeof(T), 4 / sizeof(T))
 kv8_store_kernel(const __grid_constant__ Kv8StoreArgs a) {
+  constexpr int kStoreThreads = 256 * sizeof(T);
   constexpr int kPer = 16 / sizeof(T);              // elements of a 16-byte piece
   constexpr int kPieces = kRow8 / kPer;             // pieces of a row
   constexpr int kLoads = 64 * kPieces / kStoreThreads;
@@ -155,9 +156,9 @@ cudaError_t launch_kv8_store(const Kv8StoreArgs& a_in, bool f32, int num_sms, cu
   a.rows_per_cta = min(64, max(1, a.n_rows / (4 * num_sms)));
   const int grid = (a.n_rows + a.rows_per_cta - 1) / a.rows_per_cta;
   if (f32)
-    kv8_store_kernel<float><<<grid, kStoreThreads, 0, stream>>>(a);
+    kv8_store_kernel<float><<<grid, 1024, 0, stream>>>(a);
   else
-    kv8_store_kernel<__nv_bfloat16><<<grid, kStoreThreads, 0, stream>>>(a);
+    kv8_store_kernel<__nv_bfloat16><<<grid, 512, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

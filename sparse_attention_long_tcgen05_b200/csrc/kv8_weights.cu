@@ -59,7 +59,7 @@ kv8_weights_kernel(const __grid_constant__ Kv8WeightArgs wa, const uint8_t* imag
     report(a.status, DSA_ERR_CUDA);
     return;
   }
-  const Kv8Range range = kv8_range<C::kThreads>(a.keys, a.idx != nullptr, a.k, blockIdx.x, gridDim.x, S.scratch);
+  const Kv8Range range = kv8_range<C::kThreads>(a.keys, a.idx != nullptr, a.k, blockIdx.x, gridDim.x, false, S.scratch);
   if (range.t0 == range.t1) return;
   if (threadIdx.x == 0) {
     S.ring.init();
