@@ -293,6 +293,30 @@ __device__ __forceinline__ Kv8Range kv8_range(const KeySide& ks, bool sparse, in
   return r;
 }
 
+// One query's part of a worker's range.
+struct Kv8Piece {
+  int qi, j0, n, tiles;     // tiles [j0, j0 + n) of the query's `tiles`
+};
+
+struct Kv8Pieces {
+  const Kv8AttnArgs& a;
+  int64_t left;
+  int qi, j0;
+  __device__ Kv8Pieces(const Kv8AttnArgs& args, const Kv8Range& r)
+      : a(args), left(r.t1 - r.t0), qi(r.qi), j0(r.j0) {}
+  __device__ __forceinline__ bool next(Kv8Piece& p) {
+    if (left <= 0) return false;
+    p.qi = qi;
+    p.j0 = j0;
+    p.tiles = kv8_tiles(a.keys, a.idx != nullptr, a.k, qi);
+    p.n = static_cast<int>(min(left, static_cast<int64_t>(p.tiles - j0)));
+    left -= p.n;
+    ++qi;
+    j0 = 0;
+    return true;
+  }
+};
+
 // ------------------------------------------------------------------ queries as two e4m3 terms
 
 // Writes the queries of ROWS heads (of which `live` exist) as the image of a B operand: row

@@ -62,84 +62,127 @@ struct Kv8Gather {
   int lane, g;             // g: copying warp 0..3
   uint32_t n_chunk = 0, n_rope = 0, n_tile = 0;
 
-  // Key position of this lane's row in tile j of query qi: p in [0, pos], or -1;
-  // bad: an entry past the query's position.
-  __device__ __forceinline__ int key_of(int qi, int pos, int j, bool& bad) const {
-    const int r = j * kTile + 32 * g + lane;
-    if (a.idx == nullptr) return r <= pos ? r : -1;
-    const int e = r < a.k ? __ldg(a.idx + static_cast<int64_t>(qi) * a.ld_idx + r) : -1;
-    bad = e > pos;
-    return e > pos ? -1 : e;
-  }
+  // What is known of this lane's key in one of the coming tiles: the selection's
+  // entry as it stands (or the position), and the query it belongs to.
+  struct Entry {
+    int raw, seq, pos;
+    bool live;             // there is such a tile
+  };
 
-  // Tiles [j0, j0 + n) of query qi. False when a wait ran out.
-  __device__ bool run(int qi, int j0, int n) {
-    int seq, pos;
-    const bool q_ok = kv8_query(a.keys, qi, seq, pos);
-    if (!q_ok && lane == 0) report(a.status, DSA_ERR_DEVICE_BOUNDS);
-    bool bad = false, any_bad = false;
-    int p = key_of(qi, pos, j0, bad);
-    any_bad |= bad;
-    int64_t row = p >= 0 ? kv8_row(a.keys, seq, p) : -1;
-    for (int j = j0; j < j0 + n; ++j) {
-      // the next tile's entries are fetched now, its page ids below
-      bool bad_next = false;
-      const int p_next = j + 1 < j0 + n ? key_of(qi, pos, j + 1, bad_next) : -1;
-      if (p >= 0 && row < 0) any_bad = true;      // a page id out of range
+  // All tiles of the worker's range. An entry, its page id and its block's exponent
+  // depend on one another, a memory latency each: the entry is loaded three tiles
+  // ahead of its copies, the page id two, the exponent one, each used no sooner
+  // than a tile later. (Looked up within one tile they stopped the copies for
+  // 1500 cycles in each.) False when a wait ran out.
+  __device__ bool run(Kv8Pieces& pieces) {
+    bool any_bad = false;
+    Kv8Piece pc{};
+    int left = 0, j = 0, seq = 0, pos = -1;
+    auto fetch = [&](Entry& s) {
+      s.live = true;
+      if (left == 0) {
+        s.live = pieces.next(pc);
+        if (!s.live) return;
+        if (!kv8_query(a.keys, pc.qi, seq, pos)) any_bad = true;
+        left = pc.n;
+        j = pc.j0;
+      }
+      const int r = j * kTile + 32 * g + lane;
+      if (a.idx == nullptr)
+        s.raw = r <= pos ? r : -1;
+      else
+        s.raw = r < a.k ? __ldg(a.idx + static_cast<int64_t>(pc.qi) * a.ld_idx + r) : -1;
+      s.seq = seq;
+      s.pos = pos;
+      ++j;
+      --left;
+    };
+    // the key position, and the page id to come; -1: none
+    auto look_up = [&](const Entry& s, int& p) -> int {
+      p = s.live && s.raw >= 0 ? s.raw : -1;
+      if (p > s.pos) {     // past the query's position
+        any_bad = true;
+        p = -1;
+      }
+      if (!a.keys.paged || p < 0) return 0;
+      return __ldg(a.keys.block_table + static_cast<int64_t>(s.seq) * a.keys.ld_block_table + (p >> 6));
+    };
+    auto row_of = [&](int p, int page) -> int64_t {
+      if (p < 0) return -1;
+      if (!a.keys.paged) return p;
+      if (page < 0 || page >= a.keys.num_pages) {
+        any_bad = true;
+        return -1;
+      }
+      return static_cast<int64_t>(page) * 64 + (p & 63);
+    };
+    auto exp_of = [&](int64_t row) -> int { return row >= 0 ? __ldg(a.exps + (row >> 6)) : kNoKey; };
+
+    Entry s0, s1, s2, s3;
+    fetch(s0);
+    fetch(s1);
+    fetch(s2);
+    int p0, p1, p2 = -1;
+    int page0 = look_up(s0, p0), page1 = look_up(s1, p1), page2 = 0;
+    int64_t row = row_of(p0, page0), row1 = -1;
+    int e = exp_of(row), e1 = kNoKey;
+    bool live = s0.live, live1 = s1.live;
+    while (live) {
       const bool ok = row >= 0;
-      const uint8_t* src = a.kv + (ok ? row * a.ld_kv : 0);
-      const int8_t e = ok ? __ldg(a.exps + (row >> 6)) : kNoKey;
-      const uint64_t src_bits = reinterpret_cast<uint64_t>(src);
+      const uint64_t src_bits = reinterpret_cast<uint64_t>(a.kv + (ok ? row * a.ld_kv : 0));
       const uint32_t ok_mask = __ballot_sync(0xffffffffu, ok);
       // chunk copies: instruction i covers rows 4 i .. 4 i + 3 of this warp's 32
       uint64_t at[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         at[i] = __shfl_sync(0xffffffffu, src_bits, 4 * i + (lane >> 3)) + 16 * (lane & 7);
-      int64_t row_next = -1;
 #pragma unroll
-      for (int u = 0; u < 5; ++u) {
-        if (u == 4) {
-          if (!mbar_wait_warp(&ring.rope_empty, (n_rope & 1) ^ 1, a.status)) return false;
-          const uint32_t dst = smem_u32(slots.rope);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = 8 * i + (lane >> 2);
-            const uint64_t s = __shfl_sync(0xffffffffu, src_bits, rr) + 512 + 16 * (lane & 3);
-            const int r = 32 * g + rr;
-            cp_async16_or_zero(dst + r * 64 + ((((lane & 3) ^ (r >> 1)) & 3) << 4),
-                               reinterpret_cast<const void*>(s), (ok_mask >> rr) & 1u);
-          }
-          cp_async_arrive(&ring.rope_full);
-          ++n_rope;
-        } else {
-          const uint32_t slot = n_chunk % R;
-          if (!mbar_wait_warp(&ring.empty[slot], ((n_chunk / R) & 1) ^ 1, a.status)) return false;
-          if (u == 0) {
-            const uint32_t ms = n_tile % kMeta;
-            ring.key_exp[ms][32 * g + lane] = e;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ring.meta_full[ms]);
-            ++n_tile;
-          }
-          const uint32_t dst = smem_u32(slots.chunk[slot]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = 4 * i + (lane >> 3);
-            const int r = 32 * g + rr;
-            cp_async16_or_zero(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
-                               reinterpret_cast<const void*>(at[i] + 128 * u), (ok_mask >> rr) & 1u);
-          }
-          cp_async_arrive(&ring.full[slot]);
-          ++n_chunk;
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t slot = n_chunk % R;
+        if (!mbar_wait_warp(&ring.empty[slot], ((n_chunk / R) & 1) ^ 1, a.status)) return false;
+        if (u == 0) {
+          const uint32_t ms = n_tile % kMeta;
+          ring.key_exp[ms][32 * g + lane] = static_cast<int8_t>(e);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ring.meta_full[ms]);
+          ++n_tile;
         }
-        if (u == 1 && p_next >= 0) row_next = kv8_row(a.keys, seq, p_next);
+        const uint32_t dst = smem_u32(slots.chunk[slot]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 4 * i + (lane >> 3);
+          const int r = 32 * g + rr;
+          cp_async16_or_zero(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
+                             reinterpret_cast<const void*>(at[i] + 128 * u), (ok_mask >> rr) & 1u);
+        }
+        cp_async_arrive(&ring.full[slot]);
+        ++n_chunk;
+        if (u == 0) fetch(s3);
+        if (u == 1) page2 = look_up(s2, p2);
+        if (u == 2) row1 = row_of(p1, page1);
+        if (u == 3) e1 = exp_of(row1);
       }
-      p = p_next;
-      row = row_next;
-      any_bad |= bad_next;
+      if (!mbar_wait_warp(&ring.rope_empty, (n_rope & 1) ^ 1, a.status)) return false;
+      const uint32_t dst = smem_u32(slots.rope);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = 8 * i + (lane >> 2);
+        const uint64_t s = __shfl_sync(0xffffffffu, src_bits, rr) + 512 + 16 * (lane & 3);
+        const int r = 32 * g + rr;
+        cp_async16_or_zero(dst + r * 64 + ((((lane & 3) ^ (r >> 1)) & 3) << 4),
+                           reinterpret_cast<const void*>(s), (ok_mask >> rr) & 1u);
+      }
+      cp_async_arrive(&ring.rope_full);
+      ++n_rope;
+      row = row1;
+      e = e1;
+      live = live1;
+      p1 = p2;
+      page1 = page2;
+      live1 = s2.live;
+      s2 = s3;
     }
-    if (any_bad) report(a.status, DSA_ERR_DEVICE_BOUNDS);
+    if (__any_sync(0xffffffffu, any_bad) && lane == 0) report(a.status, DSA_ERR_DEVICE_BOUNDS);
     return true;
   }
 

@@ -165,8 +165,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
   if (warp > kPvWarp) {
     // ------------------------------------------------------------ copies
     Kv8Gather<Ring> g{S.ring, S.slots, a, lane, warp - kPvWarp - 1};
-    while (pieces.next(pc))
-      if (!g.run(pc.qi, pc.j0, pc.n)) break;
+    g.run(pieces);
     g.drain();
   } else if (warp == kQkWarp) {
     // ------------------------------------------------------------ S^T = K Q^T

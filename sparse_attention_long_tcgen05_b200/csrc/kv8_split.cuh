@@ -1,35 +1,11 @@
 // kv8_split.cuh -- what the two tensor-core kernels over the 8-bit latent cache
-// share besides the copies: a worker's walk over the queries, the logits' MMAs,
+// share besides the copies: a worker's logits' MMAs,
 // and dependent launches.
 #pragma once
 
 #include "kv8_gather.cuh"
 
 namespace dsa {
-
-// One query's part of a worker's range.
-struct Kv8Piece {
-  int qi, j0, n, tiles;     // tiles [j0, j0 + n) of the query's `tiles`
-};
-
-struct Kv8Pieces {
-  const Kv8AttnArgs& a;
-  int64_t left;
-  int qi, j0;
-  __device__ Kv8Pieces(const Kv8AttnArgs& args, const Kv8Range& r)
-      : a(args), left(r.t1 - r.t0), qi(r.qi), j0(r.j0) {}
-  __device__ __forceinline__ bool next(Kv8Piece& p) {
-    if (left <= 0) return false;
-    p.qi = qi;
-    p.j0 = j0;
-    p.tiles = kv8_tiles(a.keys, a.idx != nullptr, a.k, qi);
-    p.n = static_cast<int>(min(left, static_cast<int64_t>(p.tiles - j0)));
-    left -= p.n;
-    ++qi;
-    j0 = 0;
-    return true;
-  }
-};
 
 // The warp that issues S^T = K Q^T of a worker's tiles into the TMEM columns d0 + 2 NP
 // (tile & 1): M = 128 keys, N = 2 NP; four chunks of 128 columns and the 64 rope

@@ -82,8 +82,7 @@ kv8_weights_kernel(const __grid_constant__ Kv8WeightArgs wa, const uint8_t* imag
 
   if (warp > kQkWarp) {
     Kv8Gather<Ring> g{S.ring, S.slots, a, lane, warp - kQkWarp - 1};
-    while (pieces.next(pc))
-      if (!g.run(pc.qi, pc.j0, pc.n)) break;
+    g.run(pieces);
     g.drain();
   } else if (warp == kQkWarp) {
     kv8_logits<NP, R>(a, pieces, S.slots, S.ring, S.q, images, 1, 0, &S.q_full, S.s_full, S.s_empty, tmem, lane,
