@@ -48,7 +48,7 @@ struct Kv8Ring {
 };
 
 // One copying warp. Units of a tile in the order in which the MMAs want them:
-// chunks 0, 1, 2, 3, then the rope columns. Every lane's arrival on a unit's barrier is
+// the rope columns (their slot is free first), then chunks 0 to 3. Every lane's arrival on a unit's barrier is
 // made by the copy engine when that lane's copies have landed
 // (cp.async.mbarrier.arrive.noinc), so a warp only ever waits for free slots and
 // runs as far ahead as the ring allows; the MMA issuer, having waited, makes the
@@ -136,6 +136,18 @@ struct Kv8Gather {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         at[i] = __shfl_sync(0xffffffffu, src_bits, 4 * i + (lane >> 3)) + 16 * (lane & 7);
+      if (!mbar_wait_warp(&ring.rope_empty, (n_rope & 1) ^ 1, a.status)) return false;
+      const uint32_t dst_rope = smem_u32(slots.rope);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = 8 * i + (lane >> 2);
+        const uint64_t s = __shfl_sync(0xffffffffu, src_bits, rr) + 512 + 16 * (lane & 3);
+        const int r = 32 * g + rr;
+        cp_async16_or_zero(dst_rope + r * 64 + ((((lane & 3) ^ (r >> 1)) & 3) << 4),
+                           reinterpret_cast<const void*>(s), (ok_mask >> rr) & 1u);
+      }
+      cp_async_arrive(&ring.rope_full);
+      ++n_rope;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const uint32_t slot = n_chunk % R;
@@ -162,18 +174,6 @@ struct Kv8Gather {
         if (u == 2) row1 = row_of(p1, page1);
         if (u == 3) e1 = exp_of(row1);
       }
-      if (!mbar_wait_warp(&ring.rope_empty, (n_rope & 1) ^ 1, a.status)) return false;
-      const uint32_t dst = smem_u32(slots.rope);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int rr = 8 * i + (lane >> 2);
-        const uint64_t s = __shfl_sync(0xffffffffu, src_bits, rr) + 512 + 16 * (lane & 3);
-        const int r = 32 * g + rr;
-        cp_async16_or_zero(dst + r * 64 + ((((lane & 3) ^ (r >> 1)) & 3) << 4),
-                           reinterpret_cast<const void*>(s), (ok_mask >> rr) & 1u);
-      }
-      cp_async_arrive(&ring.rope_full);
-      ++n_rope;
       row = row1;
       e = e1;
       live = live1;

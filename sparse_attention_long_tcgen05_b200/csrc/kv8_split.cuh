@@ -8,7 +8,7 @@
 namespace dsa {
 
 // The warp that issues S^T = K Q^T of a worker's tiles into the TMEM columns d0 + 2 NP
-// (tile & 1): M = 128 keys, N = 2 NP; four chunks of 128 columns and the 64 rope
+// (tile & 1): M = 128 keys, N = 2 NP; the 64 rope columns and four chunks of 128
 // columns of each tile. taken(slot) is called by the issuing lane after a
 // chunk's MMAs. images: the queries' operands (kv8_q8_kernel).
 template <int NP, int R, typename Ring, typename F>
@@ -41,16 +41,26 @@ __device__ __forceinline__ void kv8_logits(const Kv8AttnArgs& a, Kv8Pieces& piec
     for (int j = 0; j < pc.n && ok; ++j, ++g) {
       const uint32_t d = d0 + (g & 1) * (2 * NP);
       ok = mbar_wait_warp(&s_empty[g & 1], ((g >> 1) & 1) ^ 1, a.status);
+      ok = ok && mbar_wait_warp(&ring.rope_full, g & 1, a.status);
+      fence_proxy_async_smem();                      // the copies, before the MMAs read them
+      tc_fence_after();
+      if (ok && elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) mma_f8(d, r_desc + 2 * k, qr_desc + 2 * k, idesc, k != 0);
+        mma_commit(&ring.rope_empty);
+      }
+      __syncwarp();
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         ok = ok && mbar_wait_warp(&ring.full[slot], phase, a.status);
-        fence_proxy_async_smem();                    // the copies, before the MMAs read them
+        fence_proxy_async_smem();
         tc_fence_after();
         const uint64_t kd = k_desc + slot * (kChunkB / 16), qd = q_desc + c * (2 * NP * 128 / 16);
         if (ok && elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f8(d, kd + 2 * k, qd + 2 * k, idesc, (c | k) != 0);
+          for (int k = 0; k < 4; ++k) mma_f8(d, kd + 2 * k, qd + 2 * k, idesc, 1);
           taken(slot);
+          if (c == 3) mma_commit(&s_full[g & 1]);
         }
         __syncwarp();
         if (++slot == R) {
@@ -58,16 +68,6 @@ __device__ __forceinline__ void kv8_logits(const Kv8AttnArgs& a, Kv8Pieces& piec
           phase ^= 1;
         }
       }
-      ok = ok && mbar_wait_warp(&ring.rope_full, g & 1, a.status);
-      fence_proxy_async_smem();
-      tc_fence_after();
-      if (ok && elect_one()) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) mma_f8(d, r_desc + 2 * k, qr_desc + 2 * k, idesc, 1);
-        mma_commit(&s_full[g & 1]);
-        mma_commit(&ring.rope_empty);
-      }
-      __syncwarp();
     }
   }
 }
