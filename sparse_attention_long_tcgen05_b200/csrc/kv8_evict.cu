@@ -51,7 +51,7 @@ __device__ __forceinline__ uint32_t warp_before(uint32_t v, int lane, uint32_t& 
   return inc - v;
 }
 
-__global__ void __cluster_dims__(kKeepCtas, 1, 1) __launch_bounds__(kKeepThreads)
+__global__ void __cluster_dims__(kKeepCtas, 1, 1) __launch_bounds__(kKeepThreads, 2)
 kv8_keep_kernel(const __grid_constant__ Kv8EvictArgs a) {
   __shared__ __align__(16) uint32_t hist[2048];
   __shared__ uint32_t warp_sum[kKeepThreads / 32];
@@ -90,6 +90,19 @@ kv8_keep_kernel(const __grid_constant__ Kv8EvictArgs a) {
   const int lo = min(a.sink + rank * per, n - a.recent), hi = min(lo + per, n - a.recent);
   const uint32_t hist_addr = smem_u32(hist), count_addr = smem_u32(s_count);
 
+  // f(i, weight) of each of them, eight loads at a time
+  auto each = [&](auto f) {
+    for (int i0 = lo + tid; i0 < hi; i0 += 8 * kKeepThreads) {
+      float x[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+        if (i0 + t * kKeepThreads < hi) x[t] = __ldg(acc + i0 + t * kKeepThreads);
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+        if (i0 + t * kKeepThreads < hi) f(i0 + t * kKeepThreads, x[t]);
+    }
+  };
+
   // the mid-th largest key, 11 + 11 + 10 bits from the top
   uint32_t prefix = 0, left = mid;
   for (int pass = 0; pass < 3; ++pass) {
@@ -99,16 +112,12 @@ kv8_keep_kernel(const __grid_constant__ Kv8EvictArgs a) {
     if (tid == 0) s_zero = 0;
     __syncthreads();
     uint32_t zeros = 0;
-    for (int i0 = lo; i0 < hi; i0 += kKeepThreads) {
-      const int i = i0 + tid;
-      const float x = i < hi ? acc[i] : 1.f;
+    each([&](int, float x) {
       zeros += x == 0.f;
-      if (i < hi && x != 0.f) {
-        const uint32_t key = weight_key(x);
-        if (pass == 0 || (key >> (shift + bits)) == prefix)
-          atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
-      }
-    }
+      const uint32_t key = weight_key(x);
+      if (x != 0.f && (pass == 0 || (key >> (shift + bits)) == prefix))
+        atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
+    });
     zeros = __reduce_add_sync(0xffffffffu, zeros);
     if (lane == 0) atomicAdd(&s_zero, zeros);
     __syncthreads();
@@ -149,11 +158,11 @@ kv8_keep_kernel(const __grid_constant__ Kv8EvictArgs a) {
   // keys above the prefix stay, and the first `left` keys equal to it: how many of
   // both lie before this CTA's positions
   uint32_t n_gt = 0, n_eq = 0;
-  for (int i = lo + tid; i < hi; i += kKeepThreads) {
-    const uint32_t key = weight_key(acc[i]);
+  each([&](int, float x) {
+    const uint32_t key = weight_key(x);
     n_gt += key > prefix;
     n_eq += key == prefix;
-  }
+  });
   if (tid < 2) s_count[tid] = 0;
   __syncthreads();
   n_gt = __reduce_add_sync(0xffffffffu, n_gt);

@@ -157,7 +157,6 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  griddep_wait();                                    // the queries' operands
   const uint32_t tmem = S.tmem_base;
   Kv8Pieces pieces(a, range);
   Kv8Piece pc;
@@ -169,6 +168,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
     g.drain();
   } else if (warp == kQkWarp) {
     // ------------------------------------------------------------ S^T = K Q^T
+    griddep_wait();                                  // the queries' operands
     kv8_logits<NP, R>(a, pieces, S.slots, S.ring, S.q, part.images, groups, group, &S.q_full, S.s_full, S.s_empty,
                       tmem + C::kColS, lane, [](uint32_t) {});
     // nothing is in flight when the block ends, whichever way it got here
@@ -209,6 +209,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
     mbar_wait_warp(&S.drained, 0, a.status);
   } else {
     // ------------------------------------------------------------ softmax and epilogue
+    griddep_wait();                                  // the queries' factors
     const int sub = warp & 3;
     const int key = 32 * sub + lane;                 // this thread's key of each tile
     const int hb = (warp >> 2) * HN;                 // first of this warp's heads
@@ -596,7 +597,7 @@ cudaError_t launch(const Kv8AttnArgs& a, const Split& s, const Partials& part, c
   cudaError_t e = cudaFuncSetAttribute(kv8_mqa_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  constexpr int kWarps = NP / 4;                     // four heads a warp
+  constexpr int kWarps = NP <= 32 ? NP : NP / 4;     // one head a warp where there are few, else four
   kv8_q8_kernel<NP, kWarps><<<a.keys.n_q * s.groups, 32 * kWarps, 0, stream>>>(
       a.q, a.ld_q, a.heads, s.groups, s.group_heads, a.scale_log2, part.images, part.factors);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -9,23 +9,25 @@
 // One CTA owns a block from its first new row on, so no two CTAs write one
 // block and nothing is exchanged. CTA c looks at rows [c R, (c+1) R) for the
 // rows that begin a sequence's run or a block, and quantises those blocks
-// whole. The rows of a block (72 KB in bf16, up to 144 KB in fp32) stay in
-// registers between the maximum and the conversion, so each is read once: the
-// bound is HBM, 3 bytes moved per bf16 element and 5 per fp32 element.
+// whole: once over the rows for the maximum, once more (from L2) to convert
+// them. The bound is HBM, 3 bytes moved per bf16 element and 5 per fp32 element.
+// (Keeping the rows in registers between the two reads them once, but leaves an
+// SM one or two CTAs that load, then wait, then store: 38 us for the 62,000-row
+// prefill of bf16 rows, 37 us for 33,000 fp32 rows.)
 #include "kv8_common.cuh"
 
 namespace dsa {
 namespace {
 
-// Nine 16-byte pieces a thread: 512 threads for a bf16 block, two CTAs an SM, 1024
-// for an fp32 block.
+constexpr int kStoreThreads = 512;
+
 template <typename T>
-__global__ void __launch_bounds__(256 * sizeof(T), 4 / sizeof(T))
+__global__ void __launch_bounds__(kStoreThreads, 4)
 kv8_store_kernel(const __grid_constant__ Kv8StoreArgs a) {
-  constexpr int kStoreThreads = 256 * sizeof(T);
   constexpr int kPer = 16 / sizeof(T);              // elements of a 16-byte piece
   constexpr int kPieces = kRow8 / kPer;             // pieces of a row
-  constexpr int kLoads = 64 * kPieces / kStoreThreads;
+  constexpr int kBatch = 3, kLoads = 64 * kPieces / kStoreThreads;   // 9 or 18 pieces a thread
+  static_assert(kLoads % kBatch == 0, "");
   __shared__ uint32_t red[kStoreThreads / 32];
   const int tid = threadIdx.x;
   const Kv8Pages& c = a.c;
@@ -43,10 +45,14 @@ kv8_store_kernel(const __grid_constant__ Kv8StoreArgs a) {
         run0 = r;
         run1 = r + 1;
       } else {
-        int lo = 0, hi = c.n_seq;                   // the last b with cu[b] <= r
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (__ldg(a.cu + mid) <= r) lo = mid; else hi = mid;
+        // the last b with cu[b] <= r: a warp looks at 32 places at a time
+        int lo = 0, n = c.n_seq;
+        while (n > 1) {
+          const int step = (n + 31) / 32, at = (tid & 31) * step;
+          const uint32_t le = __ballot_sync(0xffffffffu, at < n && __ldg(a.cu + lo + at) <= r);
+          const int k = le != 0u ? 31 - __clz(le) : 0;
+          lo += k * step;
+          n = min(step, n - k * step);
         }
         b = lo;
         run0 = __ldg(a.cu + b);
@@ -70,24 +76,21 @@ kv8_store_kernel(const __grid_constant__ Kv8StoreArgs a) {
     const int m = static_cast<int>(min(static_cast<int64_t>(64 - slot), run1 - r));
     int64_t page = p >> 6;
     if (c.table != nullptr) page = __ldg(c.table + static_cast<int64_t>(b) * c.ld_table + (p >> 6));
-    if (page < 0 || page >= c.num_pages) {
-      if (tid == 0) report(a.status, DSA_ERR_DEVICE_BOUNDS);
-      r += m;
-      continue;
-    }
-
     const T* src = static_cast<const T*>(a.rows) + r * a.ld_rows;
-    uint4 v[kLoads];
+    auto piece = [&](int u) {                       // of the block's m rows
+      return __ldg(reinterpret_cast<const uint4*>(src + (u / kPieces) * a.ld_rows) + u % kPieces);
+    };
     uint32_t amax = 0;                              // |x| as bits: ordered like the values
+#pragma unroll 1
+    for (int i0 = 0; i0 < kLoads && i0 * kStoreThreads < m * kPieces; i0 += kBatch) {
+      uint4 v[kBatch];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int e = tid + i * kStoreThreads;
-      if (e < m * kPieces)
-        v[i] = __ldg(reinterpret_cast<const uint4*>(src + (e / kPieces) * a.ld_rows) + e % kPieces);
-    }
+      for (int i = 0; i < kBatch; ++i) {
+        const int u = tid + (i0 + i) * kStoreThreads;
+        v[i] = u < m * kPieces ? piece(u) : make_uint4(0u, 0u, 0u, 0u);
+      }
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      if (tid + i * kStoreThreads < m * kPieces) {
+      for (int i = 0; i < kBatch; ++i) {
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -97,6 +100,11 @@ kv8_store_kernel(const __grid_constant__ Kv8StoreArgs a) {
           if (x1 < 0x7f800000u) amax = max(amax, x1);
         }
       }
+    }
+    if (page < 0 || page >= c.num_pages) {
+      if (tid == 0) report(a.status, DSA_ERR_DEVICE_BOUNDS);
+      r += m;
+      continue;
     }
     amax = __reduce_max_sync(0xffffffffu, amax);
     if ((tid & 31) == 0) red[tid >> 5] = amax;
@@ -122,10 +130,18 @@ kv8_store_kernel(const __grid_constant__ Kv8StoreArgs a) {
     }
     const float f = pow2i(-e);
     uint8_t* dst = block + slot * c.ld;
+#pragma unroll 1
+    for (int i0 = 0; i0 < kLoads && i0 * kStoreThreads < m * kPieces; i0 += kBatch) {
+      uint4 v[kBatch];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int u = tid + i * kStoreThreads;
-      if (u < m * kPieces) {
+      for (int i = 0; i < kBatch; ++i) {
+        const int u = tid + (i0 + i) * kStoreThreads;
+        if (u < m * kPieces) v[i] = piece(u);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int u = tid + (i0 + i) * kStoreThreads;
+        if (u >= m * kPieces) break;
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
         uint8_t* q = dst + (u / kPieces) * c.ld + (u % kPieces) * kPer;
         if constexpr (sizeof(T) == 2) {
@@ -156,9 +172,9 @@ cudaError_t launch_kv8_store(const Kv8StoreArgs& a_in, bool f32, int num_sms, cu
   a.rows_per_cta = min(64, max(1, a.n_rows / (4 * num_sms)));
   const int grid = (a.n_rows + a.rows_per_cta - 1) / a.rows_per_cta;
   if (f32)
-    kv8_store_kernel<float><<<grid, 1024, 0, stream>>>(a);
+    kv8_store_kernel<float><<<grid, kStoreThreads, 0, stream>>>(a);
   else
-    kv8_store_kernel<__nv_bfloat16><<<grid, 512, 0, stream>>>(a);
+    kv8_store_kernel<__nv_bfloat16><<<grid, kStoreThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -75,7 +75,6 @@ kv8_weights_kernel(const __grid_constant__ Kv8WeightArgs wa, const uint8_t* imag
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  griddep_wait();                                    // the queries' operands
   const uint32_t tmem = S.tmem_base;
   Kv8Pieces pieces(a, range);
   Kv8Piece pc;
@@ -85,12 +84,14 @@ kv8_weights_kernel(const __grid_constant__ Kv8WeightArgs wa, const uint8_t* imag
     g.run(pieces);
     g.drain();
   } else if (warp == kQkWarp) {
+    griddep_wait();                                  // the queries' operands
     kv8_logits<NP, R>(a, pieces, S.slots, S.ring, S.q, images, 1, 0, &S.q_full, S.s_full, S.s_empty, tmem, lane,
                       [&](uint32_t slot) { mma_commit(&S.ring.empty[slot]); });
     if (elect_one()) mma_commit(&S.drained);
     __syncwarp();
     mbar_wait_warp(&S.drained, 0, a.status);
   } else {
+    griddep_wait();                                  // the queries' factors
     const int sub = warp & 3, grp = warp >> 2;
     const int key = 32 * sub + lane, hb = grp * HN;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * sub) << 16);
@@ -227,7 +228,7 @@ cudaError_t launch(const Kv8WeightArgs& w, int workers, uint8_t* images, float* 
   cudaError_t e = cudaFuncSetAttribute(kv8_weights_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(sizeof(Smem<NP>)));
   if (e != cudaSuccess) return e;
-  constexpr int kWarps = NP / 4;
+  constexpr int kWarps = NP <= 32 ? NP : NP / 4;     // one head a warp where there are few, else four
   kv8_q8_kernel<NP, kWarps><<<w.attn.keys.n_q, 32 * kWarps, 0, stream>>>(
       w.attn.q, w.attn.ld_q, w.attn.heads, 1, w.attn.heads, w.attn.scale_log2, images, factors);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
