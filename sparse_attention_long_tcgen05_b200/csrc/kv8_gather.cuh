@@ -65,8 +65,8 @@ struct Kv8Gather {
   // What is known of this lane's key in one of the coming tiles: the selection's
   // entry as it stands (or the position), and the query it belongs to.
   struct Entry {
-    int raw, seq, pos;
-    bool live;             // there is such a tile
+    int raw = -1, seq = 0, pos = -1;
+    bool live = false;     // there is such a tile
   };
 
   // All tiles of the worker's range. An entry, its page id and its block's exponent
@@ -100,7 +100,7 @@ struct Kv8Gather {
     // the key position, and the page id to come; -1: none
     auto look_up = [&](const Entry& s, int& p) -> int {
       p = s.live && s.raw >= 0 ? s.raw : -1;
-      if (p > s.pos) {     // past the query's position
+      if (p >= 0 && p > s.pos) {   // past the query's position
         any_bad = true;
         p = -1;
       }
