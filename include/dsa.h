@@ -373,7 +373,8 @@ DSA_API dsa_status dsa_kv8_accumulate(const dsa_attn_in* in, const int8_t* kv_ex
  * ascending, then -1; acc_out[b*ld_acc_out + 0..m-1]: their weights, later
  * columns left as they were (acc_out must not overlap acc).
  * 0 <= sink, recent; 1 <= budget, sink + recent <= budget <= 64 * ld_dst <=
- * 64 * 2^24; ld_acc >= max_pages*64; ld_kept, ld_acc_out >= budget. dst pages must
+ * 64 * 2^24, (budget / 64 + 1) * n_seq < 2^31; ld_acc >= max_pages*64; ld_kept,
+ * ld_acc_out >= budget. dst pages must
  * be distinct and none of them a page that the call reads. A length or page id
  * out of range is reported as DSA_ERR_DEVICE_BOUNDS; its sequence (length: m =
  * 0) or its rows are skipped. No workspace. */

@@ -828,6 +828,7 @@ DSA_API dsa_status dsa_kv8_accumulate(const dsa_attn_in* in, const int8_t* kv_ex
   a.lse = lse;
   a.w = static_cast<float*>(ws);
   a.n_cols = static_cast<int32_t>(cols);
+  a.n_keys = in->n_keys;
   a.decay = decay;
   a.acc = acc;
   a.ld_acc = ld_acc;
@@ -852,7 +853,8 @@ DSA_API dsa_status dsa_kv8_evict(const dsa_kv8_cache* cache, uint8_t* idx_codes,
       acc_out == nullptr || budget < 1 || sink < 0 || recent < 0 ||
       int64_t(sink) + recent > budget || ld_dst > (int64_t(1) << 24) ||
       budget > ld_dst * kPage || ld_acc < int64_t(cache->kv.max_pages) * kPage ||
-      ld_kept < budget || ld_acc_out < budget)
+      ld_kept < budget || ld_acc_out < budget ||
+      (budget / kPage + 1) * int64_t(cache->kv.n_seq) > 0x7fffffffLL)
     return DSA_ERR_INVALID_ARG;
   DeviceInfo* dev = nullptr;
   DSA_TRY(device_info(&dev));

@@ -242,6 +242,7 @@ struct Kv8WeightArgs {
   const float* lse;         // [n_q, heads]
   float* w;                 // the workspace; [n_q, n_cols]: mean over the heads
   int32_t n_cols;           // k, or the keys of the longest query
+  int32_t n_keys;           // contiguous: cached tokens
   float decay;
   float* acc;               // [n_seq, ld_acc]
   int64_t ld_acc;

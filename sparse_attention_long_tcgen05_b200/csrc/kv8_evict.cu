@@ -227,7 +227,8 @@ __global__ void __launch_bounds__(kMoveThreads)
 kv8_move_kernel(const __grid_constant__ Kv8EvictArgs a) {
   __shared__ int64_t s_row[64];
   __shared__ int s_exp[64];
-  const int b = blockIdx.x, page = blockIdx.y, tid = threadIdx.x;
+  const int pages = (a.budget + 63) / 64;
+  const int b = blockIdx.x / pages, page = blockIdx.x % pages, tid = threadIdx.x;
   griddep_wait();                                  // kept, new_lens
   const int m = min(64, a.new_lens[b] - page * 64);
   if (m <= 0) return;
@@ -294,7 +295,7 @@ cudaError_t launch_kv8_evict(const Kv8EvictArgs& a, int* launches, cudaStream_t 
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   ++*launches;
-  e = launch_dependent(kv8_move_kernel, dim3(a.c.n_seq, (a.budget + 63) / 64), kMoveThreads, 0, stream, a);
+  e = launch_dependent(kv8_move_kernel, dim3(a.c.n_seq * ((a.budget + 63) / 64)), kMoveThreads, 0, stream, a);
   if (e != cudaSuccess) return e;
   ++*launches;
   return cudaSuccess;

@@ -42,6 +42,8 @@
 // issues the logits' MMAs, one that issues the values', and four that copy. (One
 // issuing warp that polled for whichever could go on was bound by its own
 // polling: 400 cycles a unit of 4 or 8 MMAs.)
+#include <algorithm>
+
 #include "kv8_gather.cuh"
 #include "kv8_split.cuh"
 
@@ -605,30 +607,48 @@ cudaError_t launch(const Kv8AttnArgs& a, const Split& s, const Partials& part, c
                           part, s.groups, s.group_heads, s.workers, s.whole);
 }
 
+// Queries of one pass: the operands of a long prefill would otherwise need as much
+// workspace as its queries themselves. 16 queries a worker leave the last round
+// of whole queries at most 1/16 idle.
+int32_t pass_queries(int32_t n_q, int32_t heads) {
+  const int32_t most = 16 * (kMaxWorkers / ((heads + 63) / 64));
+  return n_q < most ? n_q : most;
+}
+
 }  // namespace
 
 size_t kv8_mqa_workspace(int32_t n_q, int32_t heads, int64_t max_keys, bool sparse) {
-  const Split s = split(n_q, heads, max_keys, sparse);
-  return carve(nullptr, s.whole ? 0 : s.workers, n_q, s.groups, s.np, nullptr);
+  const int32_t most = pass_queries(n_q, heads);
+  size_t bytes = 0;
+  for (const int32_t n : {most, n_q % most}) {       // full passes and the last one
+    if (n == 0) continue;
+    const Split s = split(n, heads, max_keys, sparse);
+    bytes = std::max(bytes, carve(nullptr, s.whole ? 0 : s.workers, n, s.groups, s.np, nullptr));
+  }
+  return bytes;
 }
 
-cudaError_t launch_kv8_mqa(const Kv8AttnArgs& a, int* launches, cudaStream_t stream) {
-  const int64_t max_keys = a.idx != nullptr ? a.k
-                           : a.keys.paged   ? static_cast<int64_t>(a.keys.max_pages) * 64
-                                            : a.keys.n_keys;
-  const Split s = split(a.keys.n_q, a.heads, max_keys, a.idx != nullptr);
-  Partials part;
-  carve(a.ws, s.whole ? 0 : s.workers, a.keys.n_q, s.groups, s.np, &part);
-  cudaError_t e = s.np == 16   ? launch<16>(a, s, part, stream)
-                  : s.np == 32 ? launch<32>(a, s, part, stream)
-                               : launch<64>(a, s, part, stream);
-  if (e != cudaSuccess) return e;
-  *launches += 2;
-  if (s.whole) return cudaSuccess;
-  e = launch_dependent(kv8_join_kernel, dim3(s.workers, s.groups * s.np / 4), kJoinThreads, 0, stream, a, part,
-                       s.workers, s.groups, s.group_heads, s.np);
-  if (e != cudaSuccess) return e;
-  ++*launches;
+cudaError_t launch_kv8_mqa(const Kv8AttnArgs& all, int* launches, cudaStream_t stream) {
+  const int64_t max_keys = all.idx != nullptr ? all.k
+                           : all.keys.paged   ? static_cast<int64_t>(all.keys.max_pages) * 64
+                                              : all.keys.n_keys;
+  const int32_t most = pass_queries(all.keys.n_q, all.heads);
+  for (int32_t q0 = 0; q0 < all.keys.n_q; q0 += most) {
+    const Kv8AttnArgs a = kv8_block(all, q0, std::min(most, all.keys.n_q - q0));
+    const Split s = split(a.keys.n_q, a.heads, max_keys, a.idx != nullptr);
+    Partials part;
+    carve(a.ws, s.whole ? 0 : s.workers, a.keys.n_q, s.groups, s.np, &part);
+    cudaError_t e = s.np == 16   ? launch<16>(a, s, part, stream)
+                    : s.np == 32 ? launch<32>(a, s, part, stream)
+                                 : launch<64>(a, s, part, stream);
+    if (e != cudaSuccess) return e;
+    *launches += 2;
+    if (s.whole) continue;
+    e = launch_dependent(kv8_join_kernel, dim3(s.workers, s.groups * s.np / 4), kJoinThreads, 0, stream, a, part,
+                         s.workers, s.groups, s.group_heads, s.np);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+  }
   return cudaSuccess;
 }
 

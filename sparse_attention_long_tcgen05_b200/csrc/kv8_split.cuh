@@ -72,6 +72,30 @@ __device__ __forceinline__ void kv8_logits(const Kv8AttnArgs& a, Kv8Pieces& piec
   }
 }
 
+// Queries q0 .. q0 + n - 1 of a call as a call of their own (out and lse included).
+inline Kv8AttnArgs kv8_block(const Kv8AttnArgs& all, int32_t q0, int32_t n) {
+  Kv8AttnArgs a = all;
+  KeySide& ks = a.keys;
+  a.q += q0 * all.ld_q;
+  if (a.idx != nullptr) a.idx += q0 * all.ld_idx;
+  if (a.out != nullptr) a.out += static_cast<int64_t>(q0) * all.heads * 512;
+  if (a.lse != nullptr) a.lse += static_cast<int64_t>(q0) * all.heads;
+  ks.n_q = n;
+  if (!ks.paged) {
+    ks.n_keys = all.keys.n_keys - all.keys.n_q + q0 + n;
+  } else {
+    if (ks.q_pos != nullptr) ks.q_pos += q0;
+    if (ks.q_seq != nullptr) {
+      ks.q_seq += q0;
+    } else {               // query i is sequence i
+      ks.block_table += q0 * ks.ld_block_table;
+      ks.ctx_lens += q0;
+      ks.n_seq -= q0;
+    }
+  }
+  return a;
+}
+
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // A kernel that may start while the one before it on the stream still runs

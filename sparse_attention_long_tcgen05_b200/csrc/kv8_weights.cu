@@ -16,6 +16,8 @@
 // sums do not depend on which finishes first. Within one query an entry that
 // repeats a key adds the same bits as the first, so the order of those two does
 // not matter either, and they may be added with atomics.
+#include <algorithm>
+
 #include "kv8_gather.cuh"
 #include "kv8_split.cuh"
 
@@ -165,24 +167,41 @@ kv8_weights_kernel(const __grid_constant__ Kv8WeightArgs wa, const uint8_t* imag
   }
 }
 
-// Queries of sequence b in ascending order: f(i, pos of i).
-template <typename F>
-__device__ __forceinline__ void for_queries(const KeySide& ks, int b, F f) {
-  if (ks.paged && ks.q_seq != nullptr) {
-    for (int i = 0; i < ks.n_q; ++i) {
-      int seq, pos;
-      if (__ldg(ks.q_seq + i) == b && paged_query(ks, i, seq, pos)) f(i, pos);
+// The queries of sequence b among c0 .. c0 + THREADS - 1, in ascending order, into
+// list[] = (query, position); returns how many. Executed by the whole block, which
+// meets before and after.
+template <int THREADS>
+__device__ __forceinline__ int list_queries(const KeySide& ks, int b, int c0, int2* list, int* counts) {
+  const int i = c0 + threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  bool in = false;
+  int seq, pos = -1;
+  if (i < ks.n_q) {
+    if (!ks.paged) {
+      in = true;
+      pos = ks.n_keys - ks.n_q + i;
+    } else {
+      in = (ks.q_seq != nullptr ? __ldg(ks.q_seq + i) : i) == b && paged_query(ks, i, seq, pos);
     }
-  } else if (ks.paged) {
-    int seq, pos;
-    if (b < ks.n_q && paged_query(ks, b, seq, pos)) f(b, pos);
-  } else {
-    for (int i = 0; i < ks.n_q; ++i) f(i, ks.n_keys - ks.n_q + i);
   }
+  const uint32_t votes = __ballot_sync(0xffffffffu, in);
+  __syncthreads();
+  if (lane == 0) counts[warp] = __popc(votes);
+  __syncthreads();
+  int at = 0, n = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) at += counts[w];
+    n += counts[w];
+  }
+  if (in) list[at + __popc(votes & ((1u << lane) - 1u))] = make_int2(i, pos);
+  __syncthreads();
+  return n;
 }
 
-__device__ __forceinline__ int seq_len(const KeySide& ks, int b) {
-  if (!ks.paged) return ks.n_keys;
+// Cached tokens of sequence b (all of them: a pass may see only the keys of its queries).
+__device__ __forceinline__ int seq_len(const Kv8WeightArgs& w, int b) {
+  const KeySide& ks = w.attn.keys;
+  if (!ks.paged) return w.n_keys;
   const int n = __ldg(ks.ctx_lens + b);
   return n < 0 || n > ks.max_pages * 64 ? 0 : n;
 }
@@ -190,34 +209,68 @@ __device__ __forceinline__ int seq_len(const KeySide& ks, int b) {
 // Every key of the sequence: acc = decay * acc + the queries' weights.
 __global__ void __launch_bounds__(kAccThreads)
 kv8_acc_dense_kernel(const __grid_constant__ Kv8WeightArgs w, int blocks, bool add) {
+  __shared__ int2 list[kAccThreads];
+  __shared__ int counts[kAccThreads / 32];
   griddep_wait();
   const KeySide& ks = w.attn.keys;
   const int b = blockIdx.x / blocks;
   const int s = (blockIdx.x % blocks) * kAccThreads + threadIdx.x;
-  if (s >= seq_len(ks, b)) return;
+  const bool live = s < seq_len(w, b);
   float* acc = w.acc + b * w.ld_acc + s;
-  float v = *acc * w.decay;
-  if (add)
-    for_queries(ks, b, [&](int i, int pos) {
-      if (s <= pos) v += w.w[static_cast<int64_t>(i) * w.n_cols + s];
-    });
-  *acc = v;
+  float v = live ? *acc * w.decay : 0.f;
+  if (add) {
+    const bool one = ks.paged && ks.q_seq == nullptr;          // query b alone
+    for (int c0 = one ? b / kAccThreads * kAccThreads : 0; c0 < ks.n_q; c0 += kAccThreads) {
+      const int n = list_queries<kAccThreads>(ks, b, c0, list, counts);
+#pragma unroll 4
+      for (int x = 0; x < n; ++x) {
+        const int2 q = list[x];
+        if (live && s <= q.y) v += __ldg(w.w + static_cast<int64_t>(q.x) * w.n_cols + s);
+      }
+      if (one) break;
+    }
+  }
+  if (live) *acc = v;
 }
 
-// The selected keys: query after query.
+// The selected keys: query after query, the next one's entries on their way.
 __global__ void __launch_bounds__(1024)
 kv8_acc_sparse_kernel(const __grid_constant__ Kv8WeightArgs w) {
+  __shared__ int2 list[1024];
+  __shared__ int counts[32];
   griddep_wait();
   const KeySide& ks = w.attn.keys;
-  const int b = blockIdx.x;
+  const int b = blockIdx.x, tid = threadIdx.x;
   float* acc = w.acc + b * w.ld_acc;
-  for_queries(ks, b, [&](int i, int pos) {
-    for (int j = threadIdx.x; j < w.n_cols; j += blockDim.x) {
-      const int p = __ldg(w.attn.idx + i * w.attn.ld_idx + j);
-      if (p >= 0 && p <= pos) atomicAdd(acc + p, w.w[static_cast<int64_t>(i) * w.n_cols + j]);
+  struct Part {
+    int p[2];              // (a selection has at most 2048 entries)
+    float v[2];
+  };
+  auto load = [&](int2 q) {
+    Part r;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int j = tid + 1024 * t;
+      r.p[t] = j < w.n_cols ? __ldg(w.attn.idx + q.x * w.attn.ld_idx + j) : -1;
+      r.v[t] = j < w.n_cols ? __ldg(w.w + static_cast<int64_t>(q.x) * w.n_cols + j) : 0.f;
     }
-    __syncthreads();
-  });
+    return r;
+  };
+  const bool one = ks.paged && ks.q_seq == nullptr;            // query b alone
+  for (int c0 = one ? b / 1024 * 1024 : 0; c0 < ks.n_q; c0 += 1024) {
+    const int n = list_queries<1024>(ks, b, c0, list, counts);
+    Part next = n > 0 ? load(list[0]) : Part{};
+    for (int x = 0; x < n; ++x) {
+      const Part now = next;
+      const int pos = list[x].y;
+      if (x + 1 < n) next = load(list[x + 1]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (now.p[t] >= 0 && now.p[t] <= pos) atomicAdd(acc + now.p[t], now.v[t]);
+      __syncthreads();
+    }
+    if (one) break;
+  }
 }
 
 int padded_heads(int heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : heads <= 64 ? 64 : 128; }
@@ -236,21 +289,20 @@ cudaError_t launch(const Kv8WeightArgs& w, int workers, uint8_t* images, float* 
                           static_cast<const uint8_t*>(images), static_cast<const float*>(factors));
 }
 
-}  // namespace
-
-size_t kv8_accumulate_workspace(int32_t n_q, int32_t heads, int64_t n_cols) {
-  const int np = padded_heads(heads);
-  return align256(static_cast<size_t>(n_q) * n_cols * sizeof(float)) +
-         static_cast<size_t>(n_q) * (2 * np * kRow8) + align256(static_cast<size_t>(n_q) * np * sizeof(float));
+// Queries of one pass: their weights stay within 64 MB and their operands within
+// what 2048 queries take.
+int32_t pass_queries(int32_t n_q, int64_t n_cols) {
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(2048, (int64_t(16) << 20) / n_cols));
+  return n_q < most ? n_q : static_cast<int32_t>(most);
 }
 
-cudaError_t launch_kv8_accumulate(const Kv8WeightArgs& w, int num_sms, int* launches,
-                                  cudaStream_t stream) {
+size_t weights_bytes(int32_t n, int64_t n_cols) { return align256(static_cast<size_t>(n) * n_cols * sizeof(float)); }
+
+// One pass over w's queries and n_seq sequences.
+cudaError_t pass(const Kv8WeightArgs& w, int n_seq, int num_sms, int* launches, cudaStream_t stream) {
   const KeySide& ks = w.attn.keys;
-  const int n_seq = ks.paged ? ks.n_seq : 1;
   const int np = padded_heads(w.attn.heads);
-  uint8_t* const images = reinterpret_cast<uint8_t*>(w.w) +
-                          align256(static_cast<size_t>(ks.n_q) * w.n_cols * sizeof(float));
+  uint8_t* const images = reinterpret_cast<uint8_t*>(w.w) + weights_bytes(ks.n_q, w.n_cols);
   float* const factors = reinterpret_cast<float*>(images + static_cast<size_t>(ks.n_q) * (2 * np * kRow8));
   const int64_t tiles = static_cast<int64_t>(ks.n_q) * ((w.n_cols + kTile - 1) / kTile);
   const int workers = static_cast<int>(tiles < num_sms ? tiles : num_sms);
@@ -262,16 +314,49 @@ cudaError_t launch_kv8_accumulate(const Kv8WeightArgs& w, int num_sms, int* laun
   *launches += 2;
   const bool dense = w.attn.idx == nullptr;
   if (dense || w.decay != 1.f) {
-    const int width = ks.paged ? ks.max_pages * 64 : ks.n_keys;
-    const int blocks = (width + kAccThreads - 1) / kAccThreads;
-    e = launch_dependent(kv8_acc_dense_kernel, dim3(static_cast<unsigned>(blocks) * n_seq), kAccThreads, 0, stream,
-                         w, blocks, dense);
+    const int64_t width = ks.paged ? static_cast<int64_t>(ks.max_pages) * 64 : w.n_keys;
+    const int64_t blocks = (width + kAccThreads - 1) / kAccThreads;
+    if (blocks * n_seq > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    e = launch_dependent(kv8_acc_dense_kernel, dim3(static_cast<unsigned>(blocks * n_seq)), kAccThreads, 0, stream,
+                         w, static_cast<int>(blocks), dense);
     if (e != cudaSuccess) return e;
     ++*launches;
   }
   if (!dense) {
     if ((e = launch_dependent(kv8_acc_sparse_kernel, dim3(n_seq), 1024, 0, stream, w)) != cudaSuccess) return e;
     ++*launches;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t kv8_accumulate_workspace(int32_t n_q, int32_t heads, int64_t n_cols) {
+  const int32_t n = pass_queries(n_q, n_cols);
+  const int np = padded_heads(heads);
+  return weights_bytes(n, n_cols) + static_cast<size_t>(n) * (2 * np * kRow8) +
+         align256(static_cast<size_t>(n) * np * sizeof(float));
+}
+
+cudaError_t launch_kv8_accumulate(const Kv8WeightArgs& all, int num_sms, int* launches,
+                                  cudaStream_t stream) {
+  const KeySide& ks = all.attn.keys;
+  const int32_t most = pass_queries(ks.n_q, all.n_cols);
+  for (int32_t q0 = 0; q0 < ks.n_q; q0 += most) {
+    const int32_t n = std::min(most, ks.n_q - q0);
+    const bool last = q0 + n == ks.n_q;
+    Kv8WeightArgs w = all;
+    w.attn = kv8_block(all.attn, q0, n);
+    w.lse += static_cast<int64_t>(q0) * all.attn.heads;
+    int n_seq = ks.paged ? ks.n_seq : 1;
+    if (ks.paged && ks.q_seq == nullptr) {           // this pass's sequences, and in the last the rest
+      w.acc += q0 * all.ld_acc;
+      n_seq = last ? ks.n_seq - q0 : n;
+    } else if (q0 > 0) {
+      w.decay = 1.f;                                 // every sequence has decayed in the first pass
+    }
+    const cudaError_t e = pass(w, n_seq, num_sms, launches, stream);
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

@@ -452,6 +452,68 @@ def test_accumulate_contiguous_and_empty(dsa):
         assert abs(float(acc.sum()) - (n_q - (1 if k else 0))) < 1e-3 * n_q
 
 
+@pytest.mark.parametrize("several", [False, True])
+def test_more_queries_than_one_pass_takes(dsa, several):
+    """2500 decode queries: attention in passes of 1184 (128 heads), weights in
+    passes of 2048, over sequences of their own or 300 shared ones."""
+    n_q, H, k = 2500, 66, 5
+    n_seq = 300 if several else n_q
+    g = torch.Generator().manual_seed(30)
+    lens = torch.randint(1, 65, (n_seq,), generator=g).tolist()
+    p = Paged(lens, seed=31)
+    q_seq = torch.randint(0, n_seq, (n_q,), generator=g).tolist() if several else list(range(n_q))
+    q_pos = [lens[b] - 1 for b in q_seq]
+    s, t = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in (q_seq, q_pos))
+    q = _q(n_q, H, 102)
+    idx = _selection(q_pos, k, 10)
+    rows = K.values(p.codes, p.exps)
+    att = dsa.attn_in(q, p.d_codes, SCALE, 512, kv_layout=p.layout(dsa, *((s, t) if several else ())))
+    d_idx = torch.from_numpy(idx).cuda()
+    out, lse = _attend(dsa, att, p.d_exps, d_idx, k, n_q, H)
+    acc = torch.full((n_seq, p.table.shape[1] * 64), 2.0, device="cuda")
+    ws = dsa.workspace(dsa.dsa_workspace_size(dsa.DSA_OP_KV8_ACCUMULATE, None, att, 0, 0, k))
+    dsa.dsa_kv8_accumulate(att, p.d_exps, d_idx, k, lse, 0.5, acc, ws)
+    assert dsa.dsa_check_status() == 0
+    qd, want = q.double().cpu().numpy(), np.full(acc.shape, 2.0)
+    for b, n in enumerate(lens):
+        want[b, :n] = 1.0
+    refs = [[], [], []]
+    for i in range(n_q):
+        keys = idx[i][idx[i] >= 0]
+        r = rows[p.table[q_seq[i], 0] * 64 + keys]
+        o, l, pr = K.attend(qd[i], r, SCALE)
+        np.add.at(want[q_seq[i]], keys, pr.mean(axis=0))
+        for v, x in zip(refs, (o, l, pr @ np.abs(r[:, :512]))):
+            v.append(x)
+    _close(out, lse, *(np.stack(v) for v in refs), 10.0)
+    np.testing.assert_allclose(acc.double().cpu().numpy(), want, rtol=1e-4)
+
+
+def test_contiguous_weights_in_passes(dsa):
+    """600 queries over 40,000 keys without a selection: passes of 419 queries,
+    and a decay of the keys behind the first pass's."""
+    n_keys, n_q, H = 40000, 600, 1
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(n_keys, 576, generator=g, device="cuda")
+    exps = torch.full((n_keys // 64,), -6, dtype=torch.int8, device="cuda")
+    codes = (x * 64).clamp(-448, 448).to(torch.float8_e4m3fn)
+    q = torch.randn(n_q, H, 576, generator=g, device="cuda").to(torch.bfloat16)
+    att = dsa.attn_in(q, codes.view(torch.uint8), SCALE, 512)
+    _, lse = _attend(dsa, att, exps, None, 0, n_q, H)
+    acc = torch.ones(1, n_keys, device="cuda")
+    ws = dsa.workspace(dsa.dsa_workspace_size(dsa.DSA_OP_KV8_ACCUMULATE, None, att, 0, 0, 0))
+    # 419 queries' weights (at most 64 MiB) and their operands: 2 x 16 padded heads x 576 bytes + 16 factors each
+    assert ws.numel() <= (64 << 20) + 419 * (2 * 16 * 576 + 16 * 4) + 512
+    dsa.dsa_kv8_accumulate(att, exps, None, 0, lse, 0.25, acc, ws)
+    assert dsa.dsa_check_status() == 0
+    z = q[:, 0].double() @ (codes.double() / 64).T * SCALE
+    pos = torch.arange(n_keys - n_q, n_keys, device="cuda")[:, None]
+    z = z.masked_fill(torch.arange(n_keys, device="cuda")[None] > pos, -float("inf"))
+    assert torch.max((torch.logsumexp(z, 1) - lse[:, 0]).abs()) < 1e-4
+    want = 0.25 + torch.exp(z - torch.logsumexp(z, 1, keepdim=True)).sum(dim=0)
+    assert torch.max((acc[0].double() - want).abs() / want) < 1e-4
+
+
 # ------------------------------------------------------------------------------------------ eviction
 
 @pytest.mark.parametrize("lens,budget,sink,recent", [
