@@ -8,7 +8,9 @@
 // smallest kept key and how many of the keys equal to it stay (the ones of
 // lowest position), and a last pass writes the kept positions in order. A
 // cluster of eight CTAs shares a sequence, an eighth of its positions each, and
-// adds its histograms and counts through distributed shared memory. Weights of
+// adds its histograms and counts through distributed shared memory; where no
+// sequence can be longer than 8192 tokens one CTA does it alone, which saves the
+// cluster's barriers. Weights of
 // exactly zero, which most tokens of a long sequence may have, are counted by
 // ballots: as atomics they would all go to one address.
 // Move (kv8_move_kernel): a CTA per new page copies its 64 rows; the page's
@@ -20,7 +22,7 @@
 namespace dsa {
 namespace {
 
-constexpr int kKeepThreads = 512, kKeepCtas = 8;
+constexpr int kKeepThreads = 512;
 constexpr int kMoveThreads = 256;
 
 // Larger weight, larger key; -0 = +0; NaN below every number.
@@ -51,26 +53,36 @@ __device__ __forceinline__ uint32_t warp_before(uint32_t v, int lane, uint32_t& 
   return inc - v;
 }
 
-__global__ void __cluster_dims__(kKeepCtas, 1, 1) __launch_bounds__(kKeepThreads, 2)
+// A barrier of the CTAs that share a sequence.
+template <int CTAS>
+__device__ __forceinline__ void meet() {
+  if constexpr (CTAS > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+}
+
+template <int CTAS>
+__global__ void __launch_bounds__(kKeepThreads, 2)
 kv8_keep_kernel(const __grid_constant__ Kv8EvictArgs a) {
   __shared__ __align__(16) uint32_t hist[2048];
   __shared__ uint32_t warp_sum[kKeepThreads / 32];
   __shared__ uint32_t s_prefix, s_left, s_zero, s_count[2];
-  const int b = blockIdx.x / kKeepCtas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = static_cast<int>(cluster_ctarank());
+  const int b = blockIdx.x / CTAS, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = CTAS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   griddep_launch_dependents();
   int n = a.c.ctx_lens[b];
   if (n < 0 || n > a.c.max_pages * 64) {
     if (tid == 0 && rank == 0) report(a.status, DSA_ERR_DEVICE_BOUNDS);
     n = 0;
   }
-  cluster_sync();                                  // new_lens may be ctx_lens
+  meet<CTAS>();                                  // new_lens may be ctx_lens
   if (tid == 0 && rank == 0) a.new_lens[b] = min(n, a.budget);
   int32_t* const kept = a.kept + b * a.ld_kept;
   float* const acc_out = a.acc_out + b * a.ld_acc_out;
   const float* const acc = a.acc + b * a.ld_acc;
   const int mid = a.budget - a.sink - a.recent;    // kept between sink and recent
-  const int first = rank * kKeepThreads + tid, step = kKeepCtas * kKeepThreads;
+  const int first = rank * kKeepThreads + tid, step = CTAS * kKeepThreads;
   if (n <= a.budget) {
     for (int i = first; i < a.budget; i += step) {
       kept[i] = i < n ? i : -1;
@@ -86,7 +98,7 @@ kv8_keep_kernel(const __grid_constant__ Kv8EvictArgs a) {
   }
   if (mid == 0) return;
   // this CTA's positions [lo, hi)
-  const int per = (n - a.recent - a.sink + kKeepCtas - 1) / kKeepCtas;
+  const int per = (n - a.recent - a.sink + CTAS - 1) / CTAS;
   const int lo = min(a.sink + rank * per, n - a.recent), hi = min(lo + per, n - a.recent);
   const uint32_t hist_addr = smem_u32(hist), count_addr = smem_u32(s_count);
 
@@ -125,13 +137,14 @@ kv8_keep_kernel(const __grid_constant__ Kv8EvictArgs a) {
       const uint32_t key = weight_key(0.f);
       if (pass == 0 || (key >> (shift + bits)) == prefix) hist[(key >> shift) & ((1u << bits) - 1u)] += s_zero;
     }
-    cluster_sync();
+    meet<CTAS>();
     // four bins a thread, summed over the cluster, the highest bins in thread 0
     const int bin0 = 2044 - 4 * tid;
     uint4 h = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-    for (int r = 0; r < kKeepCtas; ++r) {
-      const uint4 v = ld_cluster_v4(mapa_shared(hist_addr + 4 * bin0, r));
+    for (int r = 0; r < CTAS; ++r) {
+      const uint4 v = CTAS > 1 ? ld_cluster_v4(mapa_shared(hist_addr + 4 * bin0, r))
+                               : *reinterpret_cast<const uint4*>(hist + bin0);
       h.x += v.x;
       h.y += v.y;
       h.z += v.z;
@@ -150,7 +163,7 @@ kv8_keep_kernel(const __grid_constant__ Kv8EvictArgs a) {
       s_prefix = (prefix << bits) | static_cast<uint32_t>(bin0 + 3 - d);
       s_left = left - before;
     }
-    cluster_sync();                                // (also: the histograms have been read)
+    meet<CTAS>();                                // (also: the histograms have been read)
     prefix = s_prefix;
     left = s_left;
   }
@@ -171,7 +184,7 @@ kv8_keep_kernel(const __grid_constant__ Kv8EvictArgs a) {
     atomicAdd(&s_count[0], n_gt);
     atomicAdd(&s_count[1], n_eq);
   }
-  cluster_sync();
+  meet<CTAS>();
   uint32_t base = 0, base_eq = 0;
   for (int r = 0; r < rank; ++r) {
     const uint32_t at = mapa_shared(count_addr, r);
@@ -220,7 +233,7 @@ kv8_keep_kernel(const __grid_constant__ Kv8EvictArgs a) {
     base += total & 0xffffu;
     base_eq += total >> 16;
   }
-  cluster_sync();                                  // no CTA leaves while its counts may be read
+  meet<CTAS>();                                  // no CTA leaves while its counts may be read
 }
 
 __global__ void __launch_bounds__(kMoveThreads)
@@ -291,8 +304,23 @@ kv8_move_kernel(const __grid_constant__ Kv8EvictArgs a) {
 }  // namespace
 
 cudaError_t launch_kv8_evict(const Kv8EvictArgs& a, int* launches, cudaStream_t stream) {
-  kv8_keep_kernel<<<kKeepCtas * a.c.n_seq, kKeepThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (a.c.max_pages <= 8192 / 64) {                // (three of up to 3001 tokens: 14.4 us a call, 22.5 on clusters)
+    kv8_keep_kernel<1><<<a.c.n_seq, kKeepThreads, 0, stream>>>(a);
+    e = cudaGetLastError();
+  } else {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(8 * a.c.n_seq);
+    cfg.blockDim = dim3(kKeepThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 8;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kv8_keep_kernel<8>, a);
+  }
   if (e != cudaSuccess) return e;
   ++*launches;
   e = launch_dependent(kv8_move_kernel, dim3(a.c.n_seq * ((a.budget + 63) / 64)), kMoveThreads, 0, stream, a);
