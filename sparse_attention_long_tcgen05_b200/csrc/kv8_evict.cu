@@ -23,7 +23,7 @@ namespace dsa {
 namespace {
 
 constexpr int kKeepThreads = 512;
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 512;
 
 // Larger weight, larger key; -0 = +0; NaN below every number.
 __device__ __forceinline__ uint32_t weight_key(float x) {
@@ -236,7 +236,7 @@ kv8_keep_kernel(const __grid_constant__ Kv8EvictArgs a) {
   meet<CTAS>();                                  // no CTA leaves while its counts may be read
 }
 
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kMoveThreads, 4)
 kv8_move_kernel(const __grid_constant__ Kv8EvictArgs a) {
   __shared__ int64_t s_row[64];
   __shared__ int s_exp[64];
@@ -269,7 +269,7 @@ kv8_move_kernel(const __grid_constant__ Kv8EvictArgs a) {
   __syncthreads();
   int e = max(s_exp[tid & 31], s_exp[32 + (tid & 31)]);   // (rows past m: the minimum)
   e = __reduce_max_sync(0xffffffffu, e);
-  constexpr int kPieces = kRow8 / 16, kLoads = 64 * kPieces / kMoveThreads;
+  constexpr int kPieces = kRow8 / 16, kLoads = (64 * kPieces + kMoveThreads - 1) / kMoveThreads;
   uint4 x[kLoads];                                 // all loads before the first store
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
