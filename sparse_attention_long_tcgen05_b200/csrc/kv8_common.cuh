@@ -1,5 +1,6 @@
-// kv8_common.cuh -- e4m3 conversions and key look-up shared by the kernels of
-// the 8-bit latent cache (codes of 576-wide rows, one exponent per 64 tokens).
+// kv8_common.cuh -- what the kernels of the 8-bit latent cache (codes of 576-wide
+// rows, one exponent per 64 tokens) share: e4m3 conversions, small tensor-core
+// helpers, the split of the work, and the queries as two 8-bit terms.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -34,15 +35,6 @@ __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float f) {
   return to_e4m3x2(a.x * f, a.y * f) | (to_e4m3x2(b.x * f, b.y * f) << 16);
 }
 
-// The cached row of key position p (0 <= p <= pos) of sequence seq, or -1 when
-// its page id is out of range.
-__device__ __forceinline__ int64_t kv8_row(const KeySide& ks, int seq, int p) {
-  if (!ks.paged) return p;
-  const int pg = __ldg(ks.block_table + static_cast<int64_t>(seq) * ks.ld_block_table + (p >> 6));
-  if (pg < 0 || pg >= ks.num_pages) return -1;
-  return static_cast<int64_t>(pg) * 64 + (p & 63);
-}
-
 // Sequence and position of query qi; pos -1 when it is out of range.
 __device__ __forceinline__ bool kv8_query(const KeySide& ks, int qi, int& seq, int& pos) {
   if (ks.paged) return paged_query(ks, qi, seq, pos);
@@ -62,20 +54,6 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
   return p != 0;
-}
-
-// Whether the phase with the given parity has completed, without waiting at all
-// (try_wait suspends the warp for microseconds, whatever hint it is given).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return __all_sync(0xffffffffu, ok != 0);
 }
 
 // Descriptor of a K-major tile with 64-byte rows, 64-byte swizzle (512-byte
@@ -170,8 +148,7 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 // Four nonnegative fp16 values as sums of two e5m2 terms, a byte each. An
 // e5m2 code is the upper byte of the fp16 of its value, so the first term is
 // the value rounded to its upper byte, and what is left over, exact in fp16, is
-// rounded the same way (halves away from zero). In integer operations: the
-// conversions to 8 bits run at an eighth of their rate. A NaN is lost here.
+// rounded the same way (halves away from zero). A NaN is lost here.
 __device__ __forceinline__ void split_e5m2x4(__half2 a, __half2 b, uint32_t& hi, uint32_t& lo) {
   const uint32_t ua = (*reinterpret_cast<const uint32_t*>(&a) + 0x00800080u) & 0xff00ff00u;
   const uint32_t ub = (*reinterpret_cast<const uint32_t*>(&b) + 0x00800080u) & 0xff00ff00u;
