@@ -48,7 +48,9 @@
  *       d_v=512, V = first 512 columns of the KV row), CONTIGUOUS or PAGED
  *       with 64-token pages;
  *       F32 indexer (H_I<=64, d_I<=128, d_I%4==0) + F32 attention (H<=128,
- *       d_qk<=256, d_v<=256, separate V allowed), CONTIGUOUS only.
+ *       d_qk<=256, d_v<=256, separate V allowed), CONTIGUOUS only;
+ *       BF16 queries (1..128 heads, d_qk=576, d_v=512) over the 8-bit latent
+ *       cache: the dsa_kv8_* calls, CONTIGUOUS or PAGED with 64-token pages.
  */
 #ifndef DSA_H_
 #define DSA_H_

@@ -36,7 +36,7 @@
 // cycles at the device's 6.56 TB/s. So few heads are bound by HBM and 128 heads by
 // the tensor pipe (at 0.8 of what the bf16 rate would allow). As measured a tile of
 // 64 heads takes ~4000 cycles: with 8 slots the copies of tile g + 2 wait for the
-// values of tile g, and 1900 cycles of copy latency, the logits, 2100 cycles of
+// values of tile g, and 1900 cycles of copy latency, the logits, 2250 cycles of
 // softmax and the first value chunk of g + 2 follow one another, so two tiles take
 // ~8200. ncu: tensor pipe 51 %, issue slots 47 %, L1 62 %.
 //
