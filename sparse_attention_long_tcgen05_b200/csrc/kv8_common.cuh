@@ -18,6 +18,12 @@ constexpr int kExpMax = 63;
 // 2^e for e in [-126, 127]. Sums of two block exponents stay inside.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
+// 2^e for e in [-149, 127]: below -126 a subnormal, whose product with a value
+// large enough is exact all the same (no flushing to zero in this build).
+__device__ __forceinline__ float pow2i_wide(int e) {
+  return e >= -126 ? pow2i(e) : __int_as_float(1 << (149 + e));
+}
+
 // Two floats to e4m3 (round to nearest even, saturating, NaN kept), low byte first.
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
@@ -374,7 +380,7 @@ __device__ __forceinline__ void stage_q8(uint8_t* tile, const __nv_bfloat16* q, 
                              __shfl_sync(0xffffffffu, mr, 8 * r));
       const bool bad = m >= 0x7f80u;
       const int s = min(max(static_cast<int>(m >> 7) - 127 - 7, -112), 120);
-      const float f = pow2i(-s - 8);
+      const float f = pow2i_wide(-s - 8);            // (s up to 120: 2^-128)
       if (rr == r) {
         f_mine = f;
         bad_mine = bad;
