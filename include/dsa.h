@@ -157,7 +157,10 @@ typedef struct dsa_attn_in {
  * KV head that all query heads share, so this is one scale per block and head.
  * The scale is a power of two because moving a code to a larger exponent is
  * then exact except among e4m3's subnormals, so a page can be re-scaled, and
- * rows of several pages merged, without rounding them again. */
+ * rows of several pages merged, without rounding them again.
+ * An exponent outside [-64, 63] that a call has to use is reported as
+ * DSA_ERR_DEVICE_BOUNDS: attention and weights skip its block's keys, the store
+ * leaves the block as it is, eviction skips its rows. */
 typedef struct dsa_kv8_cache {
   uint8_t* codes;       /* CONTIGUOUS: [n_keys, 576]; PAGED: [num_pages, 64, 576]; 16-byte aligned */
   int64_t ld;           /* bytes between rows (>= 576, a multiple of 16) */

@@ -15,6 +15,8 @@ constexpr int kRow8 = 576;       // bytes of one cached row
 constexpr int kExpMin = -64;     // exponents of a block's scale 2^e
 constexpr int kExpMax = 63;
 
+__device__ __forceinline__ bool is_exponent(int e) { return e >= kExpMin && e <= kExpMax; }
+
 // 2^e for e in [-126, 127]. Sums of two block exponents stay inside.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 

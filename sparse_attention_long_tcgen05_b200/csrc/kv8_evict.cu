@@ -256,9 +256,10 @@ kv8_move_kernel(const __grid_constant__ Kv8EvictArgs a) {
     if (tid < m) {
       const int src = a.kept[b * a.ld_kept + page * 64 + tid];
       const int64_t pg = a.c.table[b * a.c.ld_table + (src >> 6)];
-      if (pg >= 0 && pg < a.c.num_pages) {
+      const int e_src = pg >= 0 && pg < a.c.num_pages ? a.c.exps[pg] : kExpMax + 1;
+      if (is_exponent(e_src)) {
         row = pg * 64 + (src & 63);
-        e = a.c.exps[pg];
+        e = e_src;
       } else {
         report(a.status, DSA_ERR_DEVICE_BOUNDS);
       }

@@ -9,7 +9,7 @@ namespace dsa {
 constexpr int kGatherWarps = 4;      // warp g copies keys 32 g .. 32 g + 31 of a tile
 constexpr int kChunkB = kTile * 128; // 128 columns of a tile's keys: 16 KB
 constexpr int kRopeB = kTile * 64;   // the 64 rope columns: 8 KB
-constexpr int8_t kNoKey = -128;      // key_exp of a key that does not count
+constexpr int8_t kNoKey = kExpMax + 1;   // key_exp of a key that does not count
 
 // Arrives on `bar` (one of its expected arrivals) when all copies that this
 // thread has issued have landed.
@@ -116,7 +116,13 @@ struct Kv8Gather {
       }
       return static_cast<int64_t>(page) * 64 + (p & 63);
     };
-    auto exp_of = [&](int64_t row) -> int { return row >= 0 ? __ldg(a.exps + (row >> 6)) : kNoKey; };
+    auto exp_of = [&](int64_t row) -> int {
+      if (row < 0) return kNoKey;
+      const int e = __ldg(a.exps + (row >> 6));
+      if (is_exponent(e)) return e;
+      any_bad = true;
+      return kNoKey;
+    };
 
     Entry s0, s1, s2, s3;
     fetch(s0);

@@ -106,9 +106,14 @@ kv8_store_kernel(const __grid_constant__ Kv8StoreArgs a) {
       r += m;
       continue;
     }
+    const int e_old = c.exps[page];
+    if (slot > 0 && !is_exponent(e_old)) {          // what the earlier rows stand for is not known
+      if (tid == 0) report(a.status, DSA_ERR_DEVICE_BOUNDS);
+      r += m;
+      continue;
+    }
     amax = __reduce_max_sync(0xffffffffu, amax);
     if ((tid & 31) == 0) red[tid >> 5] = amax;
-    const int e_old = c.exps[page];
     __syncthreads();
     amax = 0;
 #pragma unroll

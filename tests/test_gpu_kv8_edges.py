@@ -1,5 +1,5 @@
 """The 8-bit latent cache at the edges of its ranges, on the GPU: queries up to
-the largest bf16 value.
+the largest bf16 value, exponents that the format does not have.
 
 Where two calls must give the same bits, a power of two has only been moved from
 one factor to another. Other tolerances are those of test_gpu_kv8."""
@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from oracle import kv8_oracle as K
-from test_gpu_kv8 import Paged, _attend, _close, _q, _selection
+from test_gpu_kv8 import Paged, _attend, _close, _q, _selection, SCALE
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,59 @@ def test_queries_up_to_the_largest_bf16(dsa, H, k):
             _close(out, lse, *_expected(q.double().cpu().numpy(), sets, 0.5))
         for a, b in zip(ref, (out, lse, acc)):
             assert torch.equal(a, b), g
+
+
+@pytest.mark.parametrize("bad", [-128, -65, 64, 127])
+def test_exponents_outside_the_format(dsa, bad):
+    """The keys of a block whose exponent is none are reported and skipped, the
+    store leaves such a block as it is, eviction skips its rows."""
+    lens = [300, 200, 70]
+    p = Paged(lens, seed=42, extra=6)
+    q = _q(3, 32, 112)
+    p.exps[p.table[0, 2]] = p.exps[p.table[2, 1]] = bad
+    p.d_exps.copy_(torch.from_numpy(p.exps))
+    sets = [np.concatenate([np.arange(128), np.arange(192, 300)]), np.arange(200), np.arange(64)]
+    idx = np.full((3, 300), -1, dtype=np.int32)
+    for b, n in enumerate(lens):
+        idx[b, :n] = np.arange(n)
+    for k, d_idx in ((0, None), (300, torch.from_numpy(idx).cuda())):
+        att = dsa.attn_in(q, p.d_codes, SCALE, 512, kv_layout=p.layout(dsa))
+        out, lse = _attend(dsa, att, p.d_exps, d_idx, k, 3, 32)
+        assert dsa.dsa_check_status() == dsa.DSA_ERR_DEVICE_BOUNDS
+        qd = q.double().cpu().numpy()
+        _close(out, lse, *_expected(qd, [p.rows(b, s) for b, s in enumerate(sets)], SCALE))
+        acc = _weights(dsa, att, p.d_exps, d_idx, k, lse, 3, p.table.shape[1] * 64)
+        assert dsa.dsa_check_status() == dsa.DSA_ERR_DEVICE_BOUNDS
+        for b, s in enumerate(sets):
+            w = K.attend(qd[b], p.rows(b, s), SCALE)[2].mean(axis=0)
+            assert np.abs(acc[b, s].double().cpu().numpy() - w).max() <= 1e-3 * w.max()
+            rest = np.setdiff1d(np.arange(acc.shape[1]), s)
+            assert not acc[b, rest].any()
+    # the newest token of sequence 2 goes behind five rows of the bad block, sequence 0's into a sound one
+    rows = torch.randn(3, 576, generator=torch.Generator().manual_seed(2))
+    want_c, want_e = K.store(p.codes, p.exps, rows[:2].double().numpy(), [0, 1], [299, 199], p.table)
+    dsa.dsa_kv8_store(dsa.kv8_cache(p.d_codes, p.d_exps, p.layout(dsa)), rows.cuda())
+    assert dsa.dsa_check_status() == dsa.DSA_ERR_DEVICE_BOUNDS
+    assert np.array_equal(p.d_exps.cpu().numpy(), want_e) and np.array_equal(p.d_codes.cpu().numpy(), want_c)
+    p.codes, p.exps = want_c, want_e
+    # eviction: the rows of sequence 0's bad block are left out, the others moved
+    dst = torch.tensor([p.free[0:2], p.free[2:4], p.free[4:6]], dtype=torch.int32, device="cuda")
+    kept = torch.empty(3, 128, dtype=torch.int32, device="cuda")
+    acc = torch.rand(3, p.table.shape[1] * 64, generator=torch.Generator().manual_seed(3)).cuda()
+    acc_out, n = torch.zeros(3, 128, device="cuda"), torch.empty(3, dtype=torch.int32, device="cuda")
+    dsa.dsa_kv8_evict(dsa.kv8_cache(p.d_codes, p.d_exps, p.layout(dsa)), acc, 128, 2, 10, dst, n, kept, acc_out)
+    assert dsa.dsa_check_status() == dsa.DSA_ERR_DEVICE_BOUNDS
+    codes, exps = p.d_codes.cpu().numpy(), p.d_exps.cpu().numpy()
+    for b, (x, page) in enumerate(((0, 2), (1, None), (2, 1))):
+        keep = np.array(K.keep(acc[b].cpu().numpy(), lens[b], 128, 2, 10))
+        assert kept[b, :len(keep)].tolist() == keep.tolist()
+        for j in range(0, len(keep), 64):
+            src = keep[j:j + 64]
+            ok = src // 64 != page
+            to = int(dst[b, j // 64])
+            e = int(p.exps[p.table[b, src[ok] // 64]].max()) if ok.any() else -64
+            assert exps[to] == e
+            flat = p.table[b, src // 64].astype(np.int64) * 64 + src % 64
+            moved, _ = K.move(p.codes, p.exps, flat[ok], [to])
+            assert np.array_equal(codes[to, np.flatnonzero(ok)], moved[to, :ok.sum()])
+            assert np.array_equal(codes[to, np.flatnonzero(~ok)], p.codes[to, np.flatnonzero(~ok)])
