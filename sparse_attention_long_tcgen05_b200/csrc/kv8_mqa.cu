@@ -20,7 +20,11 @@
 //     M = 128 keys): each thread owns one key and multiplies by its scale. With
 //     z the logits in log2 units, P' = 2^(z + e - M) is what multiplies the codes;
 //     the running maximum M is taken over z + e, and the softmax sum is that of
-//     P' 2^-e, so no other rescaling is needed.
+//     P' 2^-e, so no other rescaling is needed. A row whose latent codes are all
+//     zero adds to the sum alone, and in a block that an outlier has scaled up its
+//     z + e would hide the others: it counts with the least e there is. Every other
+//     row gives the output at least 2^-18 of 448 2^(z + e), so M is never further
+//     than that above what the rows give.
 // The value product runs transposed as well, O^T = V^T P (M = 128 value columns,
 // N = heads): V^T is the key tile itself read MN-major, so each cached byte is
 // staged once and used by both products, and O of 64 heads takes 256 of the 512
@@ -129,6 +133,27 @@ inline size_t carve(void* ws, int workers, int64_t n_q, int groups, int np, Part
   return 2048 + o_bytes + ml_bytes + image_bytes + factor_bytes;
 }
 static_assert(3 * kMaxWorkers * sizeof(int32_t) <= 2048, "");
+
+// Whether the row of a tile's key (its first chunk is the ring's `unit`) has any
+// latent code other than zero: the first 16 nearly always tell. The tile's logits
+// have been computed, so its chunks have landed; they stay until its value
+// products are done. Looked at where the maximum is found anew only (1021-query
+// chunk 681 -> 688 us, 64-sequence decode 58.1 -> 58.9; the copying warps reading
+// them ahead from global memory instead: 690 and 61.6, 16 dense heads 103 -> 113).
+template <int R, typename Ring>
+__device__ __forceinline__ bool row_has_values(const Kv8Slots<R>& slots, Ring& ring, uint32_t unit, int key, int* status) {
+#pragma unroll 1
+  for (uint32_t c = 0; c < 4; ++c, ++unit) {
+    mbar_wait(&ring.full[unit % R], (unit / R) & 1, status);
+    const uint4* const row = reinterpret_cast<const uint4*>(slots.chunk[unit % R] + key * 128);
+#pragma unroll 1
+    for (uint32_t x = 0; x < 8; ++x) {
+      const uint4 v = row[x ^ (key & 7)];
+      if (((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) != 0) return true;
+    }
+  }
+  return false;
+}
 
 template <int NP>
 __global__ void __launch_bounds__(Cfg<NP>::kThreads, 1)
@@ -261,7 +286,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
         const int e_key = S.ring.key_exp[g % C::kMeta][key];
         const bool valid = e_key != kNoKey;
         const float ks = valid ? pow2i(e_key) : 0.f;
-        const uint64_t ks2 = f2_pack(ks, ks);
+        uint64_t ks2 = f2_pack(ks, ks);
         uint64_t s[HN / 2];                          // (hi + lo / 16) 2^e, two heads a word
         {
           uint32_t v[HN], w[HN];
@@ -318,7 +343,9 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
         }
         if (fresh) {
           float mine = -INFINITY;
-          const float e_add = valid ? static_cast<float>(e_key) : -INFINITY;
+          const bool none = valid && !row_has_values<R>(S.slots, S.ring, 4 * g, key, a.status);
+          if (none) ks2 = 0;                         // any finite P' does for a row without values
+          const float e_add = valid ? static_cast<float>(none ? kExpMin : e_key) : -INFINITY;
 #pragma unroll
           for (int i = 0; i < HN; ++i) {
             const float2 x = f2_unpack(s[i / 2]);

@@ -1,5 +1,6 @@
 """The 8-bit latent cache at the edges of its ranges, on the GPU: queries up to
-the largest bf16 value, exponents that the format does not have.
+the largest bf16 value, rows without latent values in blocks of a large scale,
+exponents that the format does not have.
 
 Where two calls must give the same bits, a power of two has only been moved from
 one factor to another. Other tolerances are those of test_gpu_kv8."""
@@ -66,6 +67,55 @@ def test_queries_up_to_the_largest_bf16(dsa, H, k):
             _close(out, lse, *_expected(q.double().cpu().numpy(), sets, 0.5))
         for a, b in zip(ref, (out, lse, acc)):
             assert torch.equal(a, b), g
+
+
+@pytest.mark.parametrize("H,k", [(16, 0), (128, 0), (16, 1500), (128, 1500)])
+def test_rows_without_latent_values_do_not_hide_the_others(dsa, H, k):
+    """Blocks whose scale an outlier token has raised by 2^28, so that their other
+    rows hold zero codes (of both signs; with rope codes in sequence 1), and a sink
+    with zero latent columns that takes all but e^-30 of the probability: the
+    output is that of the keys in ordinary blocks, far below the zero rows' z + e."""
+    lens = [1500, 1400, 1300, 1450]
+    p = Paged(lens, seed=41)
+    q = _q(4, H, 111)
+    q[:, :, 512] = 0.0
+    for b, blocks in ((0, (0, 9)), (1, (1, 20)), (2, (12,))):
+        for j in blocks:
+            pg = p.table[b, j]
+            p.exps[pg] += 28
+            p.codes[pg, :, :512] = np.where(np.arange(512) % 2, 0x80, 0x00)
+            if b != 1:
+                p.codes[pg, :, 512:] = 0x80
+            # the outlier: small latent codes, a logit of about -3e8 for every head
+            p.codes[pg, 17, :512] = K.encode_e4m3(K.round_e4m3(np.linspace(-3, 3, 512)))
+            p.codes[pg, 17, 512:] = 0
+            p.codes[pg, 17, 512] = 0xFE                   # -448
+    q[:3, :, 512] = 8.0
+    q[1, :, 513:] = 0.0                                   # sequence 1's rope codes count for nothing
+    for b in range(3):                                    # the other rows do not see that column
+        for j in range(-(-lens[b] // 64)):
+            rows = np.arange(64) != 17 if p.exps[p.table[b, j]] > 10 else np.full(64, True)
+            p.codes[p.table[b, j], rows, 512] = 0
+    # sequence 3: the sink, z = 30 for every head
+    pg = p.table[3, 4]
+    p.codes[pg, 40] = 0
+    p.codes[pg, 40, 512] = 0x7E                           # 448
+    for j in range(-(-lens[3] // 64)):
+        for r in range(64):
+            if (j, r) != (4, 40):
+                p.codes[p.table[3, j], r, 512] = 0
+    q[3, :, 512] = 30 / (SCALE * 448 * 2.0 ** float(p.exps[pg]))
+    p.d_codes.copy_(torch.from_numpy(p.codes))
+    p.d_exps.copy_(torch.from_numpy(p.exps))
+    idx = _selection([n - 1 for n in lens], k, 9) if k else None
+    att = dsa.attn_in(q, p.d_codes, SCALE, 512, kv_layout=p.layout(dsa))
+    out, lse = _attend(dsa, att, p.d_exps, torch.from_numpy(idx).cuda() if k else None, k, 4, H)
+    assert dsa.dsa_check_status() == 0
+    sets = [p.rows(b, idx[b][idx[b] >= 0] if k else np.arange(lens[b])) for b in range(4)]
+    qd = q.double().cpu().numpy()
+    for b in range(4):                                    # each by itself: their outputs are of different sizes
+        _close(out[b:b + 1], lse[b:b + 1], *_expected(qd[b:b + 1], sets[b:b + 1], SCALE))
+        assert torch.all(out[b].abs().amax(dim=1) > 0), b
 
 
 @pytest.mark.parametrize("bad", [-128, -65, 64, 127])
