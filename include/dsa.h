@@ -338,7 +338,9 @@ DSA_API dsa_status dsa_kv8_store(const dsa_kv8_cache* cache, int32_t rows_dtype,
  * any key gets a zero output and lse = -INFINITY. out: [n_q, heads, 512]
  * contiguous, 16-byte aligned; lse: [n_q, heads] or NULL.
  * Codes past a query's position are never read into a result, whatever they
- * hold; an infinity or NaN in a query head makes that head's output NaN.
+ * hold; an infinity or NaN in a query head makes that head's output NaN, and so
+ * does a largest logit beyond +-4e7, where fp32 has no digits left for the rest
+ * (times log2 e and with the key's exponent added: beyond +-2^26).
  * Workspace: dsa_workspace_size(DSA_OP_KV8_MQA, NULL, in, 0, 0, k) with k 0
  * for idx NULL; its contents are not kept between calls. */
 DSA_API dsa_status dsa_kv8_mqa_fwd(const dsa_attn_in* in, const int8_t* kv_exp,

@@ -68,6 +68,10 @@ constexpr int kMaxWorkers = 148;
 constexpr float kShift = 9.f;
 constexpr float kTop = 32768.f;
 constexpr float kLn2 = 0.69314718055994531f;
+// The largest |M| whose neighbours in fp32 (4 apart) still place the largest P'
+// within kTop. A head whose maximum lies past it is NaN, not a guess: holding
+// the maximum in two parts would give its one key instead, but cost every call 2 %.
+constexpr float kMostM = 67108864.f;
 
 // NP: heads of a CTA, padded. The ring takes what shared memory is left by the
 // queries (2 NP x 576 bytes) and P: the tile whose logits are computed and the
@@ -357,9 +361,10 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
           float mx = -INFINITY;
 #pragma unroll
           for (int t = 0; t < 4; ++t) mx = fmaxf(mx, S.tile_max[b][t][hb + lane % HN]);
+          if (mx > -INFINITY) mx = fmaxf(mx, -kMostM);   // (a later tile may still be inside)
           if (mx > m_used) {
             alpha = ex2(m_used - mx);
-            m_used = mx;
+            m_used = mx > kMostM ? NAN : mx;
           }
           rescale = j > 0;
           // (the four warps of these heads write the same values; without a key yet,
@@ -430,15 +435,16 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
       const int64_t slot = 2 * worker + (done.j0 == 0 ? 1 : 0);
       const float* const sums = &S.tile_max[g & 1][0][hb + lane % HN];
       const float lt = ((sums[0] + sums[NP]) + sums[2 * NP]) + sums[3 * NP];
+      const bool past = m_used == -kMostM;           // no key inside: a piece that counts for nothing, or NaN
       const float ref = m_used == -INFINITY ? 0.f : m_used - kShift;
-      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      const float inv = past ? NAN : lt == 0.f ? 0.f : 1.f / lt;
       if (sub == 0 && lane < HN && hb + lane < live) {
         const int64_t h = head0 + hb + lane;
         if (cut)
-          part.ml[(slot * groups + group) * NP + hb + lane] = make_float2(ref, lt);
+          part.ml[(slot * groups + group) * NP + hb + lane] = make_float2(ref, past ? 0.f : lt);
         else if (a.lse != nullptr)
           a.lse[static_cast<int64_t>(done.qi) * a.heads + h] =
-              lt == 0.f ? -INFINITY : (ref + log2f(lt)) * kLn2;
+              past ? NAN : lt == 0.f ? -INFINITY : (ref + log2f(lt)) * kLn2;
       }
       ok = ok && mbar_wait_warp(&S.pv_done, (g - 1) & 1, a.status);
       tc_fence_after();
@@ -557,10 +563,15 @@ kv8_join_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ P
   const int64_t head = static_cast<int64_t>(qi) * a.heads + group * group_heads + h;
   if ((warp & 3) == 0 && live) {                     // the factors, a warp a head
     float m = -INFINITY, l = 0.f;
+    bool past = false;                               // a piece all of whose keys lie below -kMostM
     for (int x = lane; x < n; x += 32) {
       const float2 ml = __ldcg(part.ml + (static_cast<int64_t>(s_slot[x]) * groups + group) * np + h);
-      if (ml.y != 0.f) m = fmaxf(m, ml.x);
+      if (ml.y != 0.f)
+        m = fmaxf(m, ml.x);
+      else
+        past |= ml.x != 0.f;
     }
+    past = __any_sync(0xffffffffu, past);
     m = warp_max(m);
     for (int x = lane; x < n; x += 32) {
       const float2 ml = __ldcg(part.ml + (static_cast<int64_t>(s_slot[x]) * groups + group) * np + h);
@@ -570,8 +581,9 @@ kv8_join_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ P
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-    if (lane == 0 && a.lse != nullptr) a.lse[head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float none = past ? NAN : 0.f;
+    if (lane == 0 && a.lse != nullptr) a.lse[head] = l == 0.f ? none - INFINITY : (m + log2f(l)) * kLn2;
+    const float inv = l == 0.f ? none : 1.f / l;
     __syncwarp();
     for (int x = lane; x < n; x += 32) s_f[hq][x] *= inv;
   }

@@ -1,6 +1,6 @@
 """The 8-bit latent cache at the edges of its ranges, on the GPU: queries up to
 the largest bf16 value, rows without latent values in blocks of a large scale,
-exponents that the format does not have.
+logits far beyond one, exponents that the format does not have.
 
 Where two calls must give the same bits, a power of two has only been moved from
 one factor to another. Other tolerances are those of test_gpu_kv8."""
@@ -38,7 +38,7 @@ def _expected(q, keysets, scale):
         got.append((o, l, p @ np.abs(rows[:, :512])))
         if len(rows):
             z = scale * (qi @ rows.T)
-            zm = max(zm, float(np.abs(z[z > z.max(axis=1, keepdims=True) - 60]).max()))
+            zm = max(zm, float(np.abs(z[z >= z.max(axis=1, keepdims=True) - 60]).max()))
     return (*(np.stack(x) for x in zip(*got)), zm)
 
 
@@ -116,6 +116,53 @@ def test_rows_without_latent_values_do_not_hide_the_others(dsa, H, k):
     for b in range(4):                                    # each by itself: their outputs are of different sizes
         _close(out[b:b + 1], lse[b:b + 1], *_expected(qd[b:b + 1], sets[b:b + 1], SCALE))
         assert torch.all(out[b].abs().amax(dim=1) > 0), b
+
+
+@pytest.mark.parametrize("H,k", [(16, 0), (128, 0), (32, 700), (128, 700)])
+def test_logits_far_beyond_one(dsa, H, k):
+    """Logits of up to 2^25, all the probability on the largest (two copies of a row
+    in blocks whose scales differ by 2^8; a zero logit among very negative ones);
+    past 2^26 fp32 has no room for the shift: NaN, unless a key inside decides."""
+    lens = [700, 301, 700]
+    p = Paged(lens, seed=43)
+    q = _q(3, H, 113)
+    q[:, :, 512], q[:, :, 0] = 512.0, 0.0
+    value = np.where(np.arange(576) % 3, 80.0, -96.0)     # of the rows that win, in units of 2^e
+    value[512], value[0] = 112.0, 0.0
+    for b in range(3):
+        for j in range(-(-lens[b] // 64)):
+            p.codes[p.table[b, j], :, 512] = 0x00 if b == 0 else 0xF6    # -224
+    e = int(p.exps[p.table[0, 5]])
+    for j, slot, shift in ((5, 60, 0), (9, 3, 8)):
+        pg = p.table[0, j]
+        p.exps[pg] = e + shift
+        if shift:
+            p.codes[pg] = 0
+        p.codes[pg, slot] = K.encode_e4m3(value * 2.0 ** -shift)
+    p.codes[p.table[1, 4], 44] = 0                        # the last token of sequence 1
+    p.codes[p.table[1, 4], 44, 0] = 0x38                  # 1.0
+    p.codes[p.table[1, 4], :44] = p.codes[p.table[1, 3], :44]
+    p.d_codes.copy_(torch.from_numpy(p.codes))
+    p.d_exps.copy_(torch.from_numpy(p.exps))
+    idx = _selection([n - 1 for n in lens], k, 11) if k else None
+    d_idx = torch.from_numpy(idx).cuda() if k else None
+    rows = [p.rows(b, np.arange(n)) for b, n in enumerate(lens)]
+    for g in (12, 18, 24, 40, 90, 118):                   # logits of about 37, 0 and -70 times 2^g
+        big = (q.float() * 2.0 ** g).to(torch.bfloat16)
+        att = dsa.attn_in(big, p.d_codes, SCALE, 512, kv_layout=p.layout(dsa))
+        out, lse = _attend(dsa, att, p.d_exps, d_idx, k, 3, H)
+        assert dsa.dsa_check_status() == 0
+        o, l, _, _ = _expected(big.double().cpu().numpy(), rows, SCALE)
+        got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        inside = (0, 1) if g < 20 else (1,)
+        for b in inside:                                  # one row's values, times weights exact to 2^-7, rounded to bf16
+            assert np.all(np.abs(got[b] - o[b]) <= (2.0 ** -8 + 2.0 ** -7) * np.abs(o[b])), (g, b)
+        assert np.all(gl[1] == 0), g
+        if g < 20:                                        # fp32 logits of |q| |k| at most: 2^-20 of that
+            norm = SCALE * np.linalg.norm(big[0].double().cpu().numpy(), axis=-1) * np.linalg.norm(value) * 2.0 ** e
+            assert np.all(np.abs(gl[0] - l[0]) <= 2.0 ** -20 * norm + 1e-6), g
+        else:
+            assert np.isnan(got[[0, 2]]).all() and np.isnan(gl[[0, 2]]).all(), g
 
 
 @pytest.mark.parametrize("bad", [-128, -65, 64, 127])
