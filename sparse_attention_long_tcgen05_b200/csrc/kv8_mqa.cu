@@ -264,7 +264,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
 
     // factor of head hb + lane % HN of a query
     auto factor = [&](int qi) {
-      return __ldg(part.factors + (static_cast<int64_t>(qi) * groups + group) * NP + hb + lane % HN);
+      return __ldcg(part.factors + (static_cast<int64_t>(qi) * groups + group) * NP + hb + lane % HN);
     };
     float next_factor = factor(pc.qi);
 

@@ -105,7 +105,7 @@ kv8_weights_kernel(const __grid_constant__ Kv8WeightArgs wa, const uint8_t* imag
     while (pieces.next(pc)) {
       named_bar_sync(1, 32 * C::kSumWarps);          // the last query's factors have been used
       for (int h = threadIdx.x; h < NP; h += 32 * C::kSumWarps) {
-        S.head_scale[h] = __ldg(factors + static_cast<int64_t>(pc.qi) * NP + h);
+        S.head_scale[h] = __ldcg(factors + static_cast<int64_t>(pc.qi) * NP + h);
         const float lse = h < a.heads ? __ldg(wa.lse + static_cast<int64_t>(pc.qi) * a.heads + h) : -INFINITY;
         S.neg_lse[h] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
       }
@@ -225,7 +225,7 @@ kv8_acc_dense_kernel(const __grid_constant__ Kv8WeightArgs w, int blocks, bool a
 #pragma unroll 4
       for (int x = 0; x < n; ++x) {
         const int2 q = list[x];
-        if (live && s <= q.y) v += __ldg(w.w + static_cast<int64_t>(q.x) * w.n_cols + s);
+        if (live && s <= q.y) v += __ldcg(w.w + static_cast<int64_t>(q.x) * w.n_cols + s);
       }
       if (one) break;
     }
@@ -252,7 +252,7 @@ kv8_acc_sparse_kernel(const __grid_constant__ Kv8WeightArgs w) {
     for (int t = 0; t < 2; ++t) {
       const int j = tid + 1024 * t;
       r.p[t] = j < w.n_cols ? __ldg(w.attn.idx + q.x * w.attn.ld_idx + j) : -1;
-      r.v[t] = j < w.n_cols ? __ldg(w.w + static_cast<int64_t>(q.x) * w.n_cols + j) : 0.f;
+      r.v[t] = j < w.n_cols ? __ldcg(w.w + static_cast<int64_t>(q.x) * w.n_cols + j) : 0.f;
     }
     return r;
   };

@@ -1,6 +1,7 @@
 """The 8-bit latent cache at the edges of its ranges, on the GPU: queries up to
 the largest bf16 value, rows without latent values in blocks of a large scale,
-logits far beyond one, exponents that the format does not have.
+logits far beyond one, exponents that the format does not have, calls in a row on
+one workspace.
 
 Where two calls must give the same bits, a power of two has only been moved from
 one factor to another. Other tolerances are those of test_gpu_kv8."""
@@ -163,6 +164,29 @@ def test_logits_far_beyond_one(dsa, H, k):
             assert np.all(np.abs(gl[0] - l[0]) <= 2.0 ** -20 * norm + 1e-6), g
         else:
             assert np.isnan(got[[0, 2]]).all() and np.isnan(gl[[0, 2]]).all(), g
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_calls_in_a_row_on_one_workspace(dsa, H):
+    """Queries of very different sizes, call after call without a pause in one
+    workspace: every call uses the operands and factors of its own queries."""
+    lens = [65, 700, 130]
+    p = Paged(lens, seed=44)
+    qs = [_q(3, H, 120 + i, gain=2.0 ** (3 * i - 6)) for i in range(5)]
+    atts = [dsa.attn_in(q, p.d_codes, SCALE, 512, kv_layout=p.layout(dsa)) for q in qs]
+    ref = [_attend(dsa, att, p.d_exps, None, 0, 3, H) for att in atts]
+    width = p.table.shape[1] * 64
+    ref_acc = [_weights(dsa, att, p.d_exps, None, 0, lse, 3, width) for att, (_, lse) in zip(atts, ref)]
+    ws = dsa.workspace(max(dsa.dsa_workspace_size(op, None, atts[0], 0, 0, 0)
+                           for op in (dsa.DSA_OP_KV8_MQA, dsa.DSA_OP_KV8_ACCUMULATE)))
+    outs = [[torch.empty_like(ref[0][0]), torch.empty_like(ref[0][1]), torch.zeros_like(ref_acc[0])] for _ in range(200)]
+    torch.cuda.synchronize()
+    for i, (out, lse, acc) in enumerate(outs):
+        dsa.dsa_kv8_mqa_fwd(atts[i % 5], p.d_exps, None, 0, out, lse, ws)
+        dsa.dsa_kv8_accumulate(atts[i % 5], p.d_exps, None, 0, lse, 1.0, acc, ws)
+    assert dsa.dsa_check_status() == 0
+    for i, (out, lse, acc) in enumerate(outs):
+        assert torch.equal(out, ref[i % 5][0]) and torch.equal(lse, ref[i % 5][1]) and torch.equal(acc, ref_acc[i % 5]), i
 
 
 @pytest.mark.parametrize("bad", [-128, -65, 64, 127])
