@@ -442,11 +442,11 @@ DSA_API dsa_status dsa_select_noalloc(const dsa_indexer_in* indexer, int32_t k, 
  * up, the kernel lets the copies and MMAs it already issued complete, frees its
  * tensor memory and returns -- the GPU context stays usable, but the results of
  * that call are invalid. No legitimate wait lasts more than microseconds.
- * This sets the bound of the lightning-indexer kernel's pipeline waits for
- * launches issued after the call (process-wide, all devices); ns <= 0 restores
- * the default of 1 second. The other kernels keep the 1 s bound. A bound far
- * below the copies' latency makes the indexer give up on purpose, which is
- * how the failure path is tested. */
+ * This sets the bound of the pipeline waits of the lightning-indexer kernel and
+ * of dsa_kv8_mqa_fwd and dsa_kv8_accumulate for launches issued after the call
+ * (process-wide, all devices); ns <= 0 restores the default of 1 second. The
+ * other kernels keep the 1 s bound. A bound far below the copies' latency makes
+ * these kernels give up on purpose, which is how the failure path is tested. */
 DSA_API dsa_status dsa_set_wait_limit_ns(int64_t ns);
 
 /* Number of kernel launches this process has issued through the library so

@@ -24,7 +24,8 @@ namespace {
 thread_local int32_t t_last_cuda_error = 0;
 std::atomic<int64_t> g_launches{0};
 
-// Bound of each pipeline wait of the indexer kernel (dsa_set_wait_limit_ns).
+// Bound of each pipeline wait of the indexer kernel and of the 8-bit cache's
+// attention and weights (dsa_set_wait_limit_ns).
 constexpr int64_t kDefaultWaitNs = 1000LL * 1000LL * 1000LL;
 std::atomic<int64_t> g_wait_ns{kDefaultWaitNs};
 
@@ -285,6 +286,7 @@ dsa::Kv8AttnArgs kv8_attn_args(const dsa_attn_in& in, const int8_t* kv_exp, cons
   a.k = idx != nullptr ? k : 0;
   a.keys = key_side(in.kv_layout, in.n_q, in.n_keys);
   a.scale_log2 = in.scale * 1.4426950408889634f;
+  a.wait_ns = static_cast<uint64_t>(g_wait_ns.load(std::memory_order_relaxed));
   a.status = dev->status;
   return a;
 }

@@ -28,9 +28,9 @@ __device__ __forceinline__ uint64_t global_ns() {
 // Default upper bound of any single wait inside a kernel. Legitimate waits in
 // these kernels last microseconds; one that reaches this bound reports
 // DSA_ERR_TIMEOUT and the waiting role gives up, so a kernel never hangs. The
-// indexer takes its pipeline bound from its launch arguments (this value
-// unless the caller set another); every kernel drains what it has in flight
-// with this bound before it exits.
+// indexer and the 8-bit cache's attention and weights take their pipeline bound
+// from their launch arguments (this value unless the caller set another); every
+// kernel drains what it has in flight with this bound before it exits.
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;
 
 // Time a waiting thread may be suspended inside one try_wait before it polls
@@ -81,19 +81,30 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity,
   return ok != 0;
 }
 
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Waits for the phase with the given parity to complete. Returns false (and
-// records DSA_ERR_TIMEOUT) if that does not happen within limit_ns; a single
-// suspension inside the wait never outlasts the limit either.
+// records DSA_ERR_TIMEOUT) if that does not happen within limit_ns. A limit below
+// the suspension hint is waited for without suspending: a shorter hint does not
+// bound the suspension.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* status,
                                           uint64_t limit_ns = kWaitLimitNs) {
   const uint32_t a = smem_u32(bar);
-  const uint32_t hint = limit_ns < kSuspendHintNs
-                            ? (limit_ns > 0 ? static_cast<uint32_t>(limit_ns) : 1u)
-                            : kSuspendHintNs;
-  if (mbar_try_wait(a, parity, hint)) return true;
+  const bool suspend = limit_ns >= kSuspendHintNs;
+  if (suspend ? mbar_try_wait(a, parity) : mbar_test_wait(a, parity)) return true;
   const uint64_t t0 = global_ns();
   while (true) {
-    if (mbar_try_wait(a, parity, hint)) return true;
+    if (suspend ? mbar_try_wait(a, parity) : mbar_test_wait(a, parity)) return true;
     if (global_ns() - t0 > limit_ns) {
       report(status, DSA_ERR_TIMEOUT);
       return false;

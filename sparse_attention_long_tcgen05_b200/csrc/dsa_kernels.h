@@ -230,6 +230,7 @@ struct Kv8AttnArgs {
   __nv_bfloat16* out;       // [n_q, heads, 512]
   float* lse;               // [n_q, heads] or null
   void* ws;
+  uint64_t wait_ns;         // bound of each pipeline wait before giving up
   int* status;
 };
 

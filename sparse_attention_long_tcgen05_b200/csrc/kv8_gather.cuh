@@ -60,6 +60,7 @@ struct Kv8Gather {
   Kv8Slots<R>& slots;
   const Kv8AttnArgs& a;
   int lane, g;             // g: copying warp 0..3
+  uint64_t wait_ns;
   uint32_t n_chunk = 0, n_rope = 0, n_tile = 0;
 
   // What is known of this lane's key in one of the coming tiles: the selection's
@@ -142,7 +143,7 @@ struct Kv8Gather {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         at[i] = __shfl_sync(0xffffffffu, src_bits, 4 * i + (lane >> 3)) + 16 * (lane & 7);
-      if (!mbar_wait_warp(&ring.rope_empty, (n_rope & 1) ^ 1, a.status)) return false;
+      if (!mbar_wait_warp(&ring.rope_empty, (n_rope & 1) ^ 1, a.status, wait_ns)) return false;
       const uint32_t dst_rope = smem_u32(slots.rope);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -157,7 +158,7 @@ struct Kv8Gather {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const uint32_t slot = n_chunk % R;
-        if (!mbar_wait_warp(&ring.empty[slot], ((n_chunk / R) & 1) ^ 1, a.status)) return false;
+        if (!mbar_wait_warp(&ring.empty[slot], ((n_chunk / R) & 1) ^ 1, a.status, wait_ns)) return false;
         if (u == 0) {
           const uint32_t ms = n_tile % kMeta;
           ring.key_exp[ms][32 * g + lane] = static_cast<int8_t>(e);

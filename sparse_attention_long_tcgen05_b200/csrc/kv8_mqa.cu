@@ -145,10 +145,12 @@ static_assert(3 * kMaxWorkers * sizeof(int32_t) <= 2048, "");
 // chunk 681 -> 688 us, 64-sequence decode 58.1 -> 58.9; the copying warps reading
 // them ahead from global memory instead: 690 and 61.6, 16 dense heads 103 -> 113).
 template <int R, typename Ring>
-__device__ __forceinline__ bool row_has_values(const Kv8Slots<R>& slots, Ring& ring, uint32_t unit, int key, int* status) {
+__device__ __forceinline__ bool row_has_values(const Kv8Slots<R>& slots, Ring& ring, uint32_t unit, int key, int* status,
+                                               uint64_t wait_ns, bool& ok) {
 #pragma unroll 1
   for (uint32_t c = 0; c < 4; ++c, ++unit) {
-    mbar_wait(&ring.full[unit % R], (unit / R) & 1, status);
+    ok = mbar_wait(&ring.full[unit % R], (unit / R) & 1, status, wait_ns);
+    if (!ok) return true;
     const uint4* const row = reinterpret_cast<const uint4*>(slots.chunk[unit % R] + key * 128);
 #pragma unroll 1
     for (uint32_t x = 0; x < 8; ++x) {
@@ -159,7 +161,8 @@ __device__ __forceinline__ bool row_has_values(const Kv8Slots<R>& slots, Ring& r
   return false;
 }
 
-template <int NP>
+// kLimitArg: the pipeline waits take their bound from a.wait_ns.
+template <int NP, bool kLimitArg>
 __global__ void __launch_bounds__(Cfg<NP>::kThreads, 1)
 kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Partials part, int groups,
                int group_heads, int workers, bool whole) {
@@ -170,6 +173,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
   Smem<NP>& S = *reinterpret_cast<Smem<NP>*>(smem_raw);
   const int warp = warp_id(), lane = threadIdx.x & 31;
   const int worker = blockIdx.x / groups, group = blockIdx.x % groups;
+  const uint64_t wait_ns = kLimitArg ? a.wait_ns : kWaitLimitNs;
   const int head0 = group * group_heads;
   const int live = min(group_heads, a.heads - head0);
   if (smem_u32(smem_raw) & 1023u) {                  // (never: nothing static lies before it)
@@ -202,14 +206,14 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
 
   if (warp > kPvWarp) {
     // ------------------------------------------------------------ copies
-    Kv8Gather<Ring> g{S.ring, S.slots, a, lane, warp - kPvWarp - 1};
+    Kv8Gather<Ring> g{S.ring, S.slots, a, lane, warp - kPvWarp - 1, wait_ns};
     g.run(pieces);
     g.drain();
   } else if (warp == kQkWarp) {
     // ------------------------------------------------------------ S^T = K Q^T
     griddep_wait();                                  // the queries' operands
     kv8_logits<NP, R>(a, pieces, S.slots, S.ring, S.q, part.images, groups, group, &S.q_full, S.s_full, S.s_empty,
-                      tmem + C::kColS, lane, [](uint32_t) {});
+                      tmem + C::kColS, lane, wait_ns, [](uint32_t) {});
     // nothing is in flight when the block ends, whichever way it got here
     if (elect_one()) mma_commit(&S.drained);
     __syncwarp();
@@ -223,7 +227,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
     bool ok = true;
     while (ok && pieces.next(pc)) {
       for (int j = 0; j < pc.n && ok; ++j, ++g) {
-        ok = mbar_wait_warp(&S.p_full, g & 1, a.status);
+        ok = mbar_wait_warp(&S.p_full, g & 1, a.status, wait_ns);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -284,8 +288,8 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
       for (int i = 0; i < HN / 2; ++i) l[i] = 0;
       for (int j = 0; j < pc.n; ++j, ++g) {
         const uint32_t b = g & 1;
-        ok = ok && mbar_wait_warp(&S.ring.meta_full[g % C::kMeta], (g / C::kMeta) & 1, a.status) &&
-             mbar_wait_warp(&S.s_full[b], (g >> 1) & 1, a.status);
+        ok = ok && mbar_wait_warp(&S.ring.meta_full[g % C::kMeta], (g / C::kMeta) & 1, a.status, wait_ns) &&
+             mbar_wait_warp(&S.s_full[b], (g >> 1) & 1, a.status, wait_ns);
         tc_fence_after();
         const int e_key = S.ring.key_exp[g % C::kMeta][key];
         const bool valid = e_key != kNoKey;
@@ -347,7 +351,9 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
         }
         if (fresh) {
           float mine = -INFINITY;
-          const bool none = valid && !row_has_values<R>(S.slots, S.ring, 4 * g, key, a.status);
+          bool landed = true;
+          const bool none = ok && valid && !row_has_values<R>(S.slots, S.ring, 4 * g, key, a.status, wait_ns, landed);
+          ok = __all_sync(0xffffffffu, landed) && ok;
           if (none) ks2 = 0;                         // any finite P' does for a row without values
           const float e_add = valid ? static_cast<float>(none ? kExpMin : e_key) : -INFINITY;
 #pragma unroll
@@ -387,7 +393,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
           split_e5m2x4(p[i], p[i + 1], hi[i / 2], lo[i / 2]);
         }
         // the value products of the tile before are done: P and O may be written
-        if (g > 0) ok = ok && mbar_wait_warp(&S.pv_done, (g - 1) & 1, a.status);
+        if (g > 0) ok = ok && mbar_wait_warp(&S.pv_done, (g - 1) & 1, a.status, wait_ns);
         if (rescale) {
           tc_fence_after();
 #pragma unroll 1
@@ -446,7 +452,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
           a.lse[static_cast<int64_t>(done.qi) * a.heads + h] =
               past ? NAN : lt == 0.f ? -INFINITY : (ref + log2f(lt)) * kLn2;
       }
-      ok = ok && mbar_wait_warp(&S.pv_done, (g - 1) & 1, a.status);
+      ok = ok && mbar_wait_warp(&S.pv_done, (g - 1) & 1, a.status, wait_ns);
       tc_fence_after();
       // O^T: lane = value column, TMEM column = head
       if (cut) {
@@ -643,14 +649,15 @@ template <int NP>
 cudaError_t launch(const Kv8AttnArgs& a, const Split& s, const Partials& part, cudaStream_t stream) {
   const size_t smem = sizeof(Smem<NP>);
   static_assert(sizeof(Smem<NP>) <= 232448, "shared memory of one CTA");
-  cudaError_t e = cudaFuncSetAttribute(kv8_mqa_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  auto kernel = a.wait_ns != kWaitLimitNs ? kv8_mqa_kernel<NP, true> : kv8_mqa_kernel<NP, false>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   constexpr int kWarps = NP <= 32 ? NP : NP / 4;     // one head a warp where there are few, else four
   kv8_q8_kernel<NP, kWarps><<<a.keys.n_q * s.groups, 32 * kWarps, 0, stream>>>(
       a.q, a.ld_q, a.heads, s.groups, s.group_heads, a.scale_log2, part.images, part.factors);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_dependent(kv8_mqa_kernel<NP>, dim3(s.workers * s.groups), Cfg<NP>::kThreads, smem, stream, a,
+  return launch_dependent(kernel, dim3(s.workers * s.groups), Cfg<NP>::kThreads, smem, stream, a,
                           part, s.groups, s.group_heads, s.workers, s.whole);
 }
 

@@ -15,7 +15,7 @@ template <int NP, int R, typename Ring, typename F>
 __device__ __forceinline__ void kv8_logits(const Kv8AttnArgs& a, Kv8Pieces& pieces, Kv8Slots<R>& slots, Ring& ring,
                                            uint8_t* q_tile, const uint8_t* images, int groups, int group,
                                            uint64_t* q_full, uint64_t* s_full, uint64_t* s_empty, uint32_t d0,
-                                           int lane, F taken) {
+                                           int lane, uint64_t wait_ns, F taken) {
   constexpr uint32_t idesc = make_idesc(2 * NP, 0, 0, 0, 0);
   const uint64_t q_desc = sw128_desc(smem_u32(q_tile), 16, 1024);
   const uint64_t qr_desc = sw64_desc(smem_u32(q_tile) + 4 * (2 * NP * 128));
@@ -26,7 +26,7 @@ __device__ __forceinline__ void kv8_logits(const Kv8AttnArgs& a, Kv8Pieces& piec
   bool ok = true;
   while (ok && pieces.next(pc)) {
     // the operand of the query, once the last one's logits are all computed
-    if (g > 0) ok = mbar_wait_warp(&s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, a.status);
+    if (g > 0) ok = mbar_wait_warp(&s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, a.status, wait_ns);
     if (!ok) break;
     if (elect_one()) {
       const uint8_t* image = images + (static_cast<int64_t>(pc.qi) * groups + group) * kQ8Bytes<NP>;
@@ -36,12 +36,14 @@ __device__ __forceinline__ void kv8_logits(const Kv8AttnArgs& a, Kv8Pieces& piec
         bulk_load(q_tile + c * (kQ8Bytes<NP> / 8), image + c * (kQ8Bytes<NP> / 8), kQ8Bytes<NP> / 8, q_full);
     }
     __syncwarp();
-    ok = mbar_wait_warp(q_full, n_piece & 1, a.status);
+    ok = mbar_wait_warp(q_full, n_piece & 1, a.status, wait_ns);
+    // (given up or not, no copy may land once the block has ended)
+    if (!ok) mbar_wait_warp(q_full, n_piece & 1, a.status);
     ++n_piece;
     for (int j = 0; j < pc.n && ok; ++j, ++g) {
       const uint32_t d = d0 + (g & 1) * (2 * NP);
-      ok = mbar_wait_warp(&s_empty[g & 1], ((g >> 1) & 1) ^ 1, a.status);
-      ok = ok && mbar_wait_warp(&ring.rope_full, g & 1, a.status);
+      ok = mbar_wait_warp(&s_empty[g & 1], ((g >> 1) & 1) ^ 1, a.status, wait_ns);
+      ok = ok && mbar_wait_warp(&ring.rope_full, g & 1, a.status, wait_ns);
       fence_proxy_async_smem();                      // the copies, before the MMAs read them
       tc_fence_after();
       if (ok && elect_one()) {
@@ -52,7 +54,7 @@ __device__ __forceinline__ void kv8_logits(const Kv8AttnArgs& a, Kv8Pieces& piec
       __syncwarp();
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        ok = ok && mbar_wait_warp(&ring.full[slot], phase, a.status);
+        ok = ok && mbar_wait_warp(&ring.full[slot], phase, a.status, wait_ns);
         fence_proxy_async_smem();
         tc_fence_after();
         const uint64_t kd = k_desc + slot * (kChunkB / 16), qd = q_desc + c * (2 * NP * 128 / 16);

@@ -47,7 +47,8 @@ struct Smem {
   uint32_t tmem_base;
 };
 
-template <int NP>
+// kLimitArg: the pipeline waits take their bound from a.wait_ns.
+template <int NP, bool kLimitArg>
 __global__ void __launch_bounds__(Cfg<NP>::kThreads, 1)
 kv8_weights_kernel(const __grid_constant__ Kv8WeightArgs wa, const uint8_t* images, const float* factors) {
   using C = Cfg<NP>;
@@ -56,6 +57,7 @@ kv8_weights_kernel(const __grid_constant__ Kv8WeightArgs wa, const uint8_t* imag
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem<NP>& S = *reinterpret_cast<Smem<NP>*>(smem_raw);
   const Kv8AttnArgs& a = wa.attn;
+  const uint64_t wait_ns = kLimitArg ? a.wait_ns : kWaitLimitNs;
   const int warp = warp_id(), lane = threadIdx.x & 31;
   if (smem_u32(smem_raw) & 1023u) {                  // (never: nothing static lies before it)
     report(a.status, DSA_ERR_CUDA);
@@ -82,12 +84,12 @@ kv8_weights_kernel(const __grid_constant__ Kv8WeightArgs wa, const uint8_t* imag
   Kv8Piece pc;
 
   if (warp > kQkWarp) {
-    Kv8Gather<Ring> g{S.ring, S.slots, a, lane, warp - kQkWarp - 1};
+    Kv8Gather<Ring> g{S.ring, S.slots, a, lane, warp - kQkWarp - 1, wait_ns};
     g.run(pieces);
     g.drain();
   } else if (warp == kQkWarp) {
     griddep_wait();                                  // the queries' operands
-    kv8_logits<NP, R>(a, pieces, S.slots, S.ring, S.q, images, 1, 0, &S.q_full, S.s_full, S.s_empty, tmem, lane,
+    kv8_logits<NP, R>(a, pieces, S.slots, S.ring, S.q, images, 1, 0, &S.q_full, S.s_full, S.s_empty, tmem, lane, wait_ns,
                       [&](uint32_t slot) { mma_commit(&S.ring.empty[slot]); });
     if (elect_one()) mma_commit(&S.drained);
     __syncwarp();
@@ -112,8 +114,8 @@ kv8_weights_kernel(const __grid_constant__ Kv8WeightArgs wa, const uint8_t* imag
       named_bar_sync(1, 32 * C::kSumWarps);
       for (int j = 0; j < pc.n; ++j, ++g) {
         const uint32_t b = g & 1;
-        ok = ok && mbar_wait_warp(&S.ring.meta_full[g % 8], (g / 8) & 1, a.status) &&
-             mbar_wait_warp(&S.s_full[b], (g >> 1) & 1, a.status);
+        ok = ok && mbar_wait_warp(&S.ring.meta_full[g % 8], (g / 8) & 1, a.status, wait_ns) &&
+             mbar_wait_warp(&S.s_full[b], (g >> 1) & 1, a.status, wait_ns);
         tc_fence_after();
         const int e_key = S.ring.key_exp[g % 8][key];
         const bool valid = e_key != kNoKey;
@@ -278,14 +280,15 @@ int padded_heads(int heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : heads
 template <int NP>
 cudaError_t launch(const Kv8WeightArgs& w, int workers, uint8_t* images, float* factors, cudaStream_t stream) {
   static_assert(sizeof(Smem<NP>) <= 232448, "shared memory of one CTA");
-  cudaError_t e = cudaFuncSetAttribute(kv8_weights_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  auto kernel = w.attn.wait_ns != kWaitLimitNs ? kv8_weights_kernel<NP, true> : kv8_weights_kernel<NP, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(sizeof(Smem<NP>)));
   if (e != cudaSuccess) return e;
   constexpr int kWarps = NP <= 32 ? NP : NP / 4;     // one head a warp where there are few, else four
   kv8_q8_kernel<NP, kWarps><<<w.attn.keys.n_q, 32 * kWarps, 0, stream>>>(
       w.attn.q, w.attn.ld_q, w.attn.heads, 1, w.attn.heads, w.attn.scale_log2, images, factors);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_dependent(kv8_weights_kernel<NP>, dim3(workers), Cfg<NP>::kThreads, sizeof(Smem<NP>), stream, w,
+  return launch_dependent(kernel, dim3(workers), Cfg<NP>::kThreads, sizeof(Smem<NP>), stream, w,
                           static_cast<const uint8_t*>(images), static_cast<const float*>(factors));
 }
 

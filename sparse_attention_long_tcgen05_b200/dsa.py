@@ -352,7 +352,8 @@ def dsa_select_noalloc(ind: _Keep, k: int, idx: torch.Tensor, stream=None):
 
 
 def dsa_set_wait_limit_ns(ns: int):
-    """Bound of the indexer kernel's pipeline waits (ns <= 0: the 1 s default)."""
+    """Bound of the pipeline waits of the indexer and of the 8-bit cache's attention
+    and weights (ns <= 0: the 1 s default)."""
     _check(LIB.dsa_set_wait_limit_ns(int(ns)), "dsa_set_wait_limit_ns")
 
 
