@@ -376,8 +376,15 @@ def _own(s):
         return s["codes"].view(torch.float8_e4m3fn), s["exps"]
     if case["op"] == "evict":
         cache = dsa.kv8_cache(s["codes"], s["exps"], _layout(dsa, s, False))
-        dsa.dsa_kv8_evict(cache, s["acc"], case["budget"], case["sink"], case["recent"], s["dst"], s["lens"],
-                          s["kept"], s["acc_out"], s.get("ik"), s.get("iks"))
+        # the new tables span the budget; those of sequences that are all well below it are shorter
+        dst, acc_out, more = s["dst"], s["acc_out"], -(-case["budget"] // PAGE) - s["dst"].shape[1]
+        if more > 0:
+            dst = torch.nn.functional.pad(dst, (0, more), value=-1)
+            acc_out = torch.nn.functional.pad(acc_out, (0, more * PAGE))
+        dsa.dsa_kv8_evict(cache, s["acc"], case["budget"], case["sink"], case["recent"], dst, s["lens"],
+                          s["kept"], acc_out, s.get("ik"), s.get("iks"))
+        if more > 0:
+            s["acc_out"].copy_(acc_out[:, :s["acc_out"].shape[1]])
         got = [s["kept"], s["lens"], s["acc_out"], s["codes"].view(torch.float8_e4m3fn), s["exps"]]
         if case["idx_keys"]:
             got += [s["ik"].view(torch.float8_e4m3fn), s["iks"]]
