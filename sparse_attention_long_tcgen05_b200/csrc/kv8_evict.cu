@@ -8,11 +8,11 @@
 // smallest kept key and how many of the keys equal to it stay (the ones of
 // lowest position), and a last pass writes the kept positions in order. A
 // cluster of eight CTAs shares a sequence, an eighth of its positions each, and
-// adds its histograms and counts through distributed shared memory; where no
-// sequence can be longer than 8192 tokens one CTA does it alone, which saves the
-// cluster's barriers. Weights of
-// exactly zero, which most tokens of a long sequence may have, are counted by
-// ballots: as atomics they would all go to one address.
+// adds its histograms and counts through distributed shared memory; where the
+// tables are shorter, or the sequences many, one CTA does it alone, which saves
+// the cluster's barriers. Weights of exactly zero, which most tokens of a long
+// sequence may have, are counted by ballots: as atomics they would all go to one
+// address.
 // Move (kv8_move_kernel): a CTA per new page copies its 64 rows; the page's
 // exponent is the largest of its rows' old ones, so codes move unchanged or
 // are scaled down by a power of two. Bound: HBM, every kept row read and
@@ -304,9 +304,19 @@ kv8_move_kernel(const __grid_constant__ Kv8EvictArgs a) {
 
 }  // namespace
 
+// One CTA a sequence takes about 1.1 us more for every 1024 tokens; a cluster's barriers cost
+// 6 us, and 37 clusters fill the device, so the more sequences the later they pay.
+// Measured, one CTA / clusters, us a call with the move, tables of the given tokens:
+//   1 sequence:    12288  21.5 / 22.5    16384  27.1 / 22.7    32768   38.9 / 24.6
+//   16 sequences:  16384  28.7 / 32.8    24576  38.5 / 34.8    65536   89 / 43
+//   32 sequences:  16384  35.4 / 42.6    24576  45.1 / 45.0    32768   53.5 / 45.8
+//   64 sequences:  16384  44.0 / 78.6    32768  62.1 / 84.3    65536  106.5 / 98.5
+//   150 sequences:  8192  86.4 / 201     16384  158 / 263
+constexpr int32_t kOnePages = 192, kOnePagesASeq = 8;
+
 cudaError_t launch_kv8_evict(const Kv8EvictArgs& a, int* launches, cudaStream_t stream) {
   cudaError_t e;
-  if (a.c.max_pages <= 8192 / 64) {                // (three of up to 3001 tokens: 14.4 us a call, 22.5 on clusters)
+  if (a.c.max_pages <= kOnePages + int64_t(kOnePagesASeq) * a.c.n_seq) {
     kv8_keep_kernel<1><<<a.c.n_seq, kKeepThreads, 0, stream>>>(a);
     e = cudaGetLastError();
   } else {

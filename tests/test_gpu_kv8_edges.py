@@ -1,7 +1,7 @@
 """The 8-bit latent cache at the edges of its ranges, on the GPU: queries up to
 the largest bf16 value, rows without latent values in blocks of a large scale,
 logits far beyond one, exponents that the format does not have, calls in a row on
-one workspace.
+one workspace, evictions of many ragged sequences.
 
 Where two calls must give the same bits, a power of two has only been moved from
 one factor to another. Other tolerances are those of test_gpu_kv8."""
@@ -187,6 +187,49 @@ def test_calls_in_a_row_on_one_workspace(dsa, H):
     assert dsa.dsa_check_status() == 0
     for i, (out, lse, acc) in enumerate(outs):
         assert torch.equal(out, ref[i % 5][0]) and torch.equal(lse, ref[i % 5][1]) and torch.equal(acc, ref_acc[i % 5]), i
+
+
+@pytest.mark.parametrize("lens,budget,sink,recent", [
+    ([20000, 100, 15001, 9000, 0, 5, 9001], 9000, 64, 512),       # a cluster a sequence, some within the budget
+    ([20000, 19999, 64, 0, 300], 128, 0, 0), ([17000] * 3, 16999, 3, 5),
+    ([700 + 37 * i for i in range(40)] + [0, 12000], 640, 16, 100)])   # one CTA a sequence
+def test_eviction_of_many_ragged_sequences(dsa, lens, budget, sink, recent):
+    """Selection by clusters and by single CTAs: kept positions, weights and rows of
+    sequences far above the budget, within it, and without a token."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    m = [min(n, budget) for n in lens]
+    pages, need = [-(-n // 64) for n in lens], [-(-n // 64) for n in m]
+    total = sum(pages) + sum(need)
+    perm = torch.randperm(total, generator=torch.Generator().manual_seed(7)).to(torch.int32)
+    table = torch.full((len(lens), max(pages)), -1, dtype=torch.int32)
+    dst = torch.full((len(lens), -(-budget // 64)), -1, dtype=torch.int32)
+    off = 0
+    for b in range(len(lens)):
+        table[b, :pages[b]] = perm[off:off + pages[b]]
+        dst[b, :need[b]] = perm[off + pages[b]:off + pages[b] + need[b]]
+        off += pages[b] + need[b]
+    codes = torch.randint(0, 256, (total, 64, 576), generator=g, device="cuda").to(torch.uint8) & 0xF7
+    exps = torch.full((total,), -6, dtype=torch.int8, device="cuda")
+    acc = torch.rand(len(lens), table.shape[1] * 64, generator=g, device="cuda") ** 4
+    acc[torch.rand(acc.shape, generator=g, device="cuda") < 0.4] = 0.0
+    before = codes.clone()
+    ctx = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    n = torch.full_like(ctx, -7)
+    kept = torch.full((len(lens), budget), -7, dtype=torch.int32, device="cuda")
+    acc_out = torch.full((len(lens), budget), -7.0, device="cuda")
+    cache = dsa.kv8_cache(codes, exps, dsa.paged_layout(table.cuda(), ctx, total))
+    dsa.dsa_kv8_evict(cache, acc, budget, sink, recent, dst.cuda(), n, kept, acc_out)
+    assert dsa.dsa_check_status() == 0
+    assert n.tolist() == m
+    want = before.cpu()
+    for b in range(len(lens)):
+        w = acc[b].cpu().numpy()
+        keep = np.array(K.keep(w, lens[b], budget, sink, recent), dtype=np.int64)
+        assert np.array_equal(kept[b].cpu().numpy(), np.concatenate([keep, np.full(budget - len(keep), -1)])), b
+        assert np.array_equal(acc_out[b, :len(keep)].cpu().numpy(), w[keep]) and (acc_out[b, len(keep):] == -7).all(), b
+        at = np.arange(len(keep))
+        want[dst[b].numpy()[at // 64], at % 64] = before.cpu()[table[b].numpy()[keep // 64], keep % 64]
+    assert torch.equal(codes.cpu(), want)
 
 
 @pytest.mark.parametrize("bad", [-128, -65, 64, 127])
