@@ -211,6 +211,8 @@ def attn_in(q, kv, scale, d_v, v=None, kv_layout: Optional[KvLayout] = None):
     if kv.dtype is not torch.uint8:
         return _Keep(s, [q, kv, v])
     # the 8-bit cache
+    if not paged and kv.dim() != 2:
+        raise DsaError(DSA_ERR_INVALID_ARG, "attn_in: kv must be [n_keys, 576] without a paged layout")
     if st[2] != 1 or (heads > 1 and st[1] != d_qk):
         raise DsaError(DSA_ERR_INVALID_ARG, "attn_in: q's heads must follow one another")
     n_seq, keys, blocks, dev = _cache_fits(lay, paged, kv, n_keys, n_q, "attn_in: kv")
@@ -225,6 +227,8 @@ def kv8_cache(codes: torch.Tensor, exps: torch.Tensor, kv: Optional[KvLayout] = 
     further apart than 576 bytes, pages not further than their 64 rows."""
     lay = kv if kv is not None else KvLayout(DSA_KV_CONTIGUOUS, 0, None, 0, 0, 0, None)
     paged = lay.kind == DSA_KV_PAGED
+    if not paged and n_keys is None and codes.dim() != 2:
+        raise DsaError(DSA_ERR_INVALID_ARG, "kv8_cache: codes must be [n_keys, 576] without a paged layout or n_keys")
     n = 0 if paged else n_keys if n_keys is not None else codes.shape[0]
     n_seq, keys, blocks, dev = _cache_fits(lay, paged, codes, n, 0, "kv8_cache: codes")
     if not (exps.dtype is _I8 and exps.numel() >= blocks and exps.is_contiguous()):

@@ -107,6 +107,12 @@ def test_contiguous_caches(dsa):
     codes, exps = torch.zeros(200, 576, dtype=torch.uint8), torch.zeros(4, dtype=torch.int8)
     dsa.kv8_cache(codes, exps)
     dsa.kv8_cache(codes.view(2, 100, 576), exps, None, 200)
+    q = torch.zeros(1, 4, 576, dtype=torch.bfloat16)
+    dsa.attn_in(q, codes, 0.1, 512)
+    for build in (lambda: dsa.kv8_cache(codes.view(2, 100, 576), exps),          # 2 keys?
+                  lambda: dsa.attn_in(q, codes.view(2, 100, 576), 0.1, 512)):
+        with pytest.raises(dsa.DsaError, match="must be .n_keys, 576."):
+            build()
     with pytest.raises(dsa.DsaError, match="200|201"):
         dsa.kv8_cache(codes, exps, None, 201)
     with pytest.raises(dsa.DsaError, match="4 contiguous"):
