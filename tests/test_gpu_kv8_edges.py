@@ -1,7 +1,7 @@
 """The 8-bit latent cache at the edges of its ranges, on the GPU: queries up to
 the largest bf16 value, rows without latent values in blocks of a large scale,
 logits far beyond one, exponents that the format does not have, calls in a row on
-one workspace, evictions of many ragged sequences.
+one workspace.
 
 Where two calls must give the same bits, a power of two has only been moved from
 one factor to another. Other tolerances are those of test_gpu_kv8."""
@@ -230,6 +230,35 @@ def test_eviction_of_many_ragged_sequences(dsa, lens, budget, sink, recent):
         at = np.arange(len(keep))
         want[dst[b].numpy()[at // 64], at % 64] = before.cpu()[table[b].numpy()[keep // 64], keep % 64]
     assert torch.equal(codes.cpu(), want)
+
+
+@pytest.mark.parametrize("H,k", [(16, 0), (128, 0), (128, 1400)])
+@pytest.mark.parametrize("shift", [9, 13, 17])
+def test_rows_far_below_their_blocks_scale(dsa, H, k, shift):
+    """Blocks that an outlier has scaled up by 2^9 to 2^17: their other rows, of
+    ordinary values, keep the small codes that are left of them, and their z + e
+    lies as far above that of the other blocks' keys, which weigh as much."""
+    lens = [1400, 1500]
+    p = Paged(lens, seed=46)
+    for b, j in ((0, 0), (1, 7)):
+        p.codes[:, :, 512:] = 0
+        pg = p.table[b, j]
+        x = K.values(p.codes, p.exps).reshape(-1, 64, 576)[pg]
+        p.exps[pg] += shift
+        p.codes[pg] = K.encode_e4m3(K.round_e4m3(x * 2.0 ** -float(p.exps[pg])))
+        p.codes[pg, 30] = K.encode_e4m3(np.full(576, 352.0))  # the outlier
+    q = _q(2, H, 114)
+    q[:, :, 512:] = -8.0                                  # only the outlier has rope codes
+    p.d_codes.copy_(torch.from_numpy(p.codes))
+    p.d_exps.copy_(torch.from_numpy(p.exps))
+    idx = _selection([n - 1 for n in lens], k, 14) if k else None
+    att = dsa.attn_in(q, p.d_codes, SCALE, 512, kv_layout=p.layout(dsa))
+    out, lse = _attend(dsa, att, p.d_exps, torch.from_numpy(idx).cuda() if k else None, k, 2, H)
+    assert dsa.dsa_check_status() == 0
+    sets = [p.rows(b, idx[b][idx[b] >= 0] if k else np.arange(lens[b])) for b in range(2)]
+    qd = q.double().cpu().numpy()
+    for b in range(2):
+        _close(out[b:b + 1], lse[b:b + 1], *_expected(qd[b:b + 1], sets[b:b + 1], SCALE))
 
 
 @pytest.mark.parametrize("bad", [-128, -65, 64, 127])
