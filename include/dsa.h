@@ -341,6 +341,13 @@ DSA_API dsa_status dsa_kv8_store(const dsa_kv8_cache* cache, int32_t rows_dtype,
  * hold; an infinity or NaN in a query head makes that head's output NaN, and so
  * does a largest logit beyond +-4e7, where fp32 has no digits left for the rest
  * (times log2 e and with the key's exponent added: beyond +-2^26).
+ * Accuracy: logits, lse and all sums are fp32, over products that are exact but
+ * for query elements below 2^-14 of their head's largest (held to 2^-22 of it).
+ * A key enters the output with its probability to 2^-7 (0.24 % in the rms) while
+ * p 2^e (e: its block's exponent) is within 2^-20 of the largest such product
+ * among the keys with any nonzero latent code, less exactly below, as zero below
+ * 2^-26 of it; the output is rounded to bf16 once. Measured against 64 bits: rms
+ * error 0.17 to 0.23 % of the output, of which that rounding is 0.17 %.
  * Workspace: dsa_workspace_size(DSA_OP_KV8_MQA, NULL, in, 0, 0, k) with k 0
  * for idx NULL; its contents are not kept between calls. */
 DSA_API dsa_status dsa_kv8_mqa_fwd(const dsa_attn_in* in, const int8_t* kv_exp,
@@ -355,7 +362,10 @@ DSA_API dsa_status dsa_kv8_mqa_fwd(const dsa_attn_in* in, const int8_t* kv_exp,
  * (its selection, or 0..pos with idx NULL; an entry that repeats a key counts
  * again). CONTIGUOUS: one sequence of n_keys. in, kv_exp, idx, k: as given to
  * dsa_kv8_mqa_fwd; lse: [n_q, heads], its log-sum-exp (a head with lse =
- * -INFINITY adds nothing). decay is finite and in [0, 1]. acc: n_seq rows
+ * -INFINITY adds nothing, one with NaN makes the weights of its query's keys
+ * NaN). The mean is over the heads of this call: where a model's heads are spread
+ * over several GPUs, acc has to be averaged over them before dsa_kv8_evict, or
+ * each of them keeps other tokens. decay is finite and in [0, 1]. acc: n_seq rows
  * (n_seq 0: n_q rows), ld_acc >= max_pages*64 (PAGED) or n_keys. The sums run
  * in a fixed order: the same call gives the same bits.
  * Workspace: dsa_workspace_size(DSA_OP_KV8_ACCUMULATE, NULL, in, 0, 0, k). */
