@@ -346,7 +346,7 @@ DSA_API dsa_status dsa_kv8_store(const dsa_kv8_cache* cache, int32_t rows_dtype,
  * A key enters the output with its probability to 2^-7 (0.24 % in the rms) while
  * p 2^e (e: its block's exponent) is within 2^-20 of the largest such product
  * among the keys with any nonzero latent code, less exactly below, as zero below
- * 2^-26 of it; the output is rounded to bf16 once. Measured against 64 bits: rms
+ * 2^-26 of it (or 2^-122 of the probability of a key without); the output is rounded to bf16 once. Measured against 64 bits: rms
  * error 0.17 to 0.23 % of the output, of which that rounding is 0.17 %.
  * Workspace: dsa_workspace_size(DSA_OP_KV8_MQA, NULL, in, 0, 0, k) with k 0
  * for idx NULL; its contents are not kept between calls. */

@@ -25,7 +25,7 @@
 //     the running maximum M is taken over z + e, and the softmax sum is that of
 //     P' 2^-e, so no other rescaling is needed. A row whose latent codes are all
 //     zero adds to the sum alone, and in a block that an outlier has scaled up its
-//     z + e would hide the others: it counts with the least e there is. Every other
+//     z + e would hide the others: it counts with an e of -96. Every other
 //     row gives the output at least 2^-18 of 448 2^(z + e), so M is never further
 //     than that above what the rows give.
 // The value product runs transposed as well, O^T = V^T P (M = 128 value columns,
@@ -70,6 +70,9 @@ constexpr int kMaxWorkers = 148;
 // maximum M is only moved when a tile exceeds it by more than 2^6.
 constexpr float kShift = 9.f;
 constexpr float kTop = 32768.f;
+// What a row without latent values has instead of its block's exponent when the
+// maximum is taken: 2^17 such rows with the largest logit then sum to 2^122.
+constexpr int kNoValuesExp = -96;
 constexpr float kLn2 = 0.69314718055994531f;
 // The largest |M| whose neighbours in fp32 (4 apart) still place the largest P'
 // within kTop. A head whose maximum lies past it is NaN, not a guess: holding
@@ -358,7 +361,7 @@ kv8_mqa_kernel(const __grid_constant__ Kv8AttnArgs a, const __grid_constant__ Pa
           const bool none = ok && valid && !row_has_values<R>(S.slots, S.ring, 4 * g, key, a.status, wait_ns, landed);
           ok = __all_sync(0xffffffffu, landed) && ok;
           if (none) ks2 = 0;                         // any finite P' does for a row without values
-          const float e_add = valid ? static_cast<float>(none ? kExpMin : e_key) : -INFINITY;
+          const float e_add = valid ? static_cast<float>(none ? kNoValuesExp : e_key) : -INFINITY;
 #pragma unroll
           for (int i = 0; i < HN; ++i) {
             const float2 x = f2_unpack(s[i / 2]);

@@ -70,11 +70,11 @@ def test_queries_up_to_the_largest_bf16(dsa, H, k):
             assert torch.equal(a, b), g
 
 
-@pytest.mark.parametrize("H,k", [(16, 0), (128, 0), (16, 1500), (128, 1500)])
-def test_rows_without_latent_values_do_not_hide_the_others(dsa, H, k):
+@pytest.mark.parametrize("H,k,sink", [(16, 0, 30), (128, 0, 70), (16, 1500, 70), (128, 1500, 30)])
+def test_rows_without_latent_values_do_not_hide_the_others(dsa, H, k, sink):
     """Blocks whose scale an outlier token has raised by 2^28, so that their other
     rows hold zero codes (of both signs; with rope codes in sequence 1), and a sink
-    with zero latent columns that takes all but e^-30 of the probability: the
+    with zero latent columns that takes all but e^-30 or e^-70 of the probability: the
     output is that of the keys in ordinary blocks, far below the zero rows' z + e."""
     lens = [1500, 1400, 1300, 1450]
     p = Paged(lens, seed=41)
@@ -97,7 +97,7 @@ def test_rows_without_latent_values_do_not_hide_the_others(dsa, H, k):
         for j in range(-(-lens[b] // 64)):
             rows = np.arange(64) != 17 if p.exps[p.table[b, j]] > 10 else np.full(64, True)
             p.codes[p.table[b, j], rows, 512] = 0
-    # sequence 3: the sink, z = 30 for every head
+    # sequence 3: the sink, the same z for every head
     pg = p.table[3, 4]
     p.codes[pg, 40] = 0
     p.codes[pg, 40, 512] = 0x7E                           # 448
@@ -105,7 +105,7 @@ def test_rows_without_latent_values_do_not_hide_the_others(dsa, H, k):
         for r in range(64):
             if (j, r) != (4, 40):
                 p.codes[p.table[3, j], r, 512] = 0
-    q[3, :, 512] = 30 / (SCALE * 448 * 2.0 ** float(p.exps[pg]))
+    q[3, :, 512] = sink / (SCALE * 448 * 2.0 ** float(p.exps[pg]))
     p.d_codes.copy_(torch.from_numpy(p.codes))
     p.d_exps.copy_(torch.from_numpy(p.exps))
     idx = _selection([n - 1 for n in lens], k, 9) if k else None
